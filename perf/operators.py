@@ -317,10 +317,9 @@ def _own(s):
         return dict(g, y=y, state_out=st)
     kw = dict(gate=s["gate"], gate_kind={"none": osr.GATE_NONE, "gelu": osr.GATE_GELU,
                                          "silu": osr.GATE_SILU}[c["gate"]],
-              post_norm=c["post"], w_post=s["w_post"], scale=s["scale"], pre_norm=c["pre"], w_pre=s["w_pre"], eps=EPS,
-              x_dtype=_DT[c["res_dtype"]])
+              post_norm=c["post"], w_post=s["w_post"], scale=s["scale"], pre_norm=c["pre"], w_pre=s["w_pre"], eps=EPS)
     if op == "norm_fwd":
-        x_out, z = osr.lattice_osr_norm_fwd(s["y"], s["x"], z_dtype=_DT[c["dtype"]], **kw)
+        x_out, z = osr.lattice_osr_norm_fwd(s["y"], s["x"], x_dtype=_DT[c["res_dtype"]], **kw)
         return {"x_out": x_out, "z": z} if c["pre"] else {"x_out": x_out}
     return osr.lattice_osr_norm_bwd(s["y"], s["x"], s["dx_out"], s["dz"], grad_dtype=_DT[c["dtype"]], **kw)
 
