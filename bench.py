@@ -75,8 +75,9 @@ def chain_reference_ms(w: dict, chunk: int) -> float:
 # Sources of the backward kernels (every csrc/osr_bwd* file): not part of the
 # forward and decode kernels whose traffic counters are keyed by the hash below.
 BWD_PREFIX = "osr_bwd"
-# Source of the layer-glue kernels: not part of either.
+# Sources of the layer-glue kernels, and (csrc/layer_*) of the scan and the norms: not part of either.
 GLUE_SOURCES = ("osr_glue.hip",)
+LAYER_PREFIX = "layer_"
 
 
 def source_hash() -> str:
@@ -84,7 +85,7 @@ def source_hash() -> str:
     h = hashlib.sha256()
     for p in sorted(glob.glob(os.path.join(ROOT, "compressed_memory_linear_amd", "csrc", "*"))):
         base = os.path.basename(p)
-        if base.startswith(BWD_PREFIX) or base in GLUE_SOURCES:
+        if base.startswith((BWD_PREFIX, LAYER_PREFIX)) or base in GLUE_SOURCES:
             continue
         with open(p, "rb") as f:
             h.update(f.read())

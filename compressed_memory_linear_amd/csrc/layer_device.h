@@ -1,0 +1,59 @@
+// layer_device.h -- device helpers shared by the layer operators' kernels:
+// vectors of V consecutive elements, and the gates.
+#pragma once
+
+#include "osr_device.h"
+
+namespace layer {
+
+// V consecutive elements as stored: V floats, or V bf16 bit patterns.
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T e[V];
+};
+
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T* p, int64_t i) {
+    return *reinterpret_cast<const Vec<T, V>*>(p + i);
+}
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(uint16_t x) { return osr::bf16_bits_to_f32(x); }
+
+// V values stored as fp32, or as bf16 (the one rounding, to nearest even).
+template <int V>
+__device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&x)[V], bool bf16) {
+    if (bf16) {
+        Vec<uint16_t, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.e[j] = osr::f32_to_bf16_bits(x[j]);
+        *reinterpret_cast<Vec<uint16_t, V>*>(static_cast<uint16_t*>(p) + i) = o;
+    } else {
+        Vec<float, V> o;
+#pragma unroll
+        for (int j = 0; j < V; ++j) o.e[j] = x[j];
+        *reinterpret_cast<Vec<float, V>*>(static_cast<float*>(p) + i) = o;
+    }
+}
+
+// e^x through the hardware's 2^x.  The product x log2(e) is kept in two parts:
+// rounded to one float it would cost a relative |x| 2^-24 of the result.
+__device__ __forceinline__ float exp_acc(float x) {
+    constexpr float kLog2e = 1.44269504088896341f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
+    const float hi = x * kLog2e;
+    // past the range of 2^x the low part is not wanted (it is NaN at infinite x)
+    const float lo = fmaf(x, kLog2eLo, fmaf(x, kLog2e, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return fabsf(hi) < 128.0f ? fmaf(e, lo * kLn2, e) : e;
+}
+
+// s = sigmoid(x) and r = 1 - s, each to a few units of 2^-24 of its own value:
+// with e = e^-x, s = 1 / (1 + e) and r = e s (1 once e is so large that s is
+// below half a unit of 1; the product would be inf 0 there).  x = -inf gives
+// s = 0, r = 1 and x = +inf gives s = 1, r = 0, exactly; NaN stays NaN.
+__device__ __forceinline__ void sigmoid2(float x, float& s, float& r) {
+    const float e = exp_acc(-x);
+    s = __builtin_amdgcn_rcpf(1.0f + e);
+    r = e > 33554432.0f ? 1.0f : e * s;
+}
+
+}  // namespace layer

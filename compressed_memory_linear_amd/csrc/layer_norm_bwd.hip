@@ -1,0 +1,232 @@
+// layer_norm_bwd.hip -- gradient of the norms around a block (layer_norm_fwd.hip).
+//
+// With n1 = u / rms(u), n = n1 w_post, xh = x' / rms(x') and the means over a row,
+//     dx' = dx_out + (t - xh mean(t xh)) / rms(x'),  t = dz w_pre,   dw_pre = sum dz xh,
+//     dx = dx',  dscale = sum dx' n,  dn = scale dx',                dw_post = sum dn n1,
+//     du = (s - n1 mean(s n1)) / rms(u),  s = dn w_post,
+//     dy = du phi(gate),  dgate = du y phi'(gate).
+// The forward is taken again from y, gate and x, which have to be read anyway,
+// so that nothing of it is kept and x' is not read back rounded.  The sums over
+// rows are held by each thread for its columns while its workgroup walks over
+// its rows; the workgroups' sums go to the workspace and are added in a fixed
+// order by a second kernel (no atomics: reruns agree bit for bit).
+#include "layer_norm.h"
+
+namespace layer {
+namespace {
+
+template <typename S, bool VEC, typename TIn, typename TRes>
+__global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
+    __shared__ float red[2][S::NT / 64][2];
+    // column sums of the workgroup's row slots (S::ROWS > 1 only)
+    __shared__ float cols[S::ROWS > 1 ? S::ROWS : 1][S::ROWS > 1 ? S::TPR * kE : 1];
+    RowSum<S, 2> sum{red};
+    const int lane = threadIdx.x % S::TPR;
+    const int sub = threadIdx.x / S::TPR;
+    const float inv = 1.0f / static_cast<float>(p.D);
+
+    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
+    float gpost[S::K][kE], gsc[S::K][kE], gpre[S::K][kE];
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
+        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
+        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) gpost[k][e] = gsc[k][e] = gpre[k][e] = 0.0f;
+    }
+    const int steps = (p.R + S::ROWS - 1) / S::ROWS;
+    for (int it = blockIdx.x; it < steps; it += gridDim.x) {
+        const int row = it * S::ROWS + sub;
+        const bool live = row < p.R;  // past the end: a row of zeros, in step with the barriers
+        const int64_t at = static_cast<int64_t>(row) * p.D;
+        float yv[S::K][kE], phi[S::K][kE], dphi[S::K][kE], xo[S::K][kE], d[S::K][kE], t[S::K][kE];
+        float ss[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            Piece<TIn> ry = {}, rg = {}, rz = {};
+            Piece<TRes> rx = {}, rd = {};
+            if (live && p.y) load_piece<S, VEC>(static_cast<const TIn*>(p.y) + at, lane, k, p.D, ry);
+            if (live && p.gate) load_piece<S, VEC>(static_cast<const TIn*>(p.gate) + at, lane, k, p.D, rg);
+            if (live && p.x) load_piece<S, VEC>(static_cast<const TRes*>(p.x) + at, lane, k, p.D, rx);
+            if (live && p.dx_out) load_piece<S, VEC>(static_cast<const TRes*>(p.dx_out) + at, lane, k, p.D, rd);
+            if (live && p.dz) load_piece<S, VEC>(static_cast<const TIn*>(p.dz) + at, lane, k, p.D, rz);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                yv[k][e] = widen(ry.e[e]);
+                xo[k][e] = widen(rx.e[e]);
+                d[k][e] = widen(rd.e[e]);
+                t[k][e] = widen(rz.e[e]);
+                phi[k][e] = 1.0f, dphi[k][e] = 0.0f;
+            }
+            if (p.gate_kind == 1) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float g = widen(rg.e[e]);
+                    const float cdf = 0.5f * erfcf(-g * 0.70710678118654752f);
+                    phi[k][e] = g * cdf;
+                    dphi[k][e] = fmaf(g * 0.39894228040143268f, exp_acc(-0.5f * g * g), cdf);
+                }
+            } else if (p.gate_kind == 2) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float g = widen(rg.e[e]);
+                    float s, r;
+                    sigmoid2(g, s, r);
+                    phi[k][e] = g * s;
+                    dphi[k][e] = s * fmaf(g, r, 1.0f);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const float u = yv[k][e] * phi[k][e];
+                ss[0] = fmaf(u, u, ss[0]);
+            }
+        }
+        float r1 = 1.0f;
+        if (p.y) {
+            if (p.post) {
+                sum(ss);
+                r1 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+            }
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e)
+                    xo[k][e] = fmaf(yv[k][e] * phi[k][e] * r1 * wpost[k][e], sc[k][e], xo[k][e]);
+        }
+        if (p.pre) {
+            ss[0] = ss[1] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    ss[0] = fmaf(xo[k][e], xo[k][e], ss[0]);
+                    ss[1] = fmaf(t[k][e] * wpre[k][e], xo[k][e], ss[1]);
+                }
+            sum(ss);
+            const float r2 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+            const float m = ss[1] * inv * r2;  // mean(t xh)
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float xh = xo[k][e] * r2;
+                    gpre[k][e] = fmaf(t[k][e], xh, gpre[k][e]);
+                    d[k][e] = fmaf(r2, fmaf(-xh, m, t[k][e] * wpre[k][e]), d[k][e]);
+                }
+        }
+        if (p.dx && live) {
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(p.dx, p.res_bf16, at, lane, k, p.D, d[k]);
+        }
+        if (!p.y) continue;
+        ss[0] = ss[1] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const float n1 = yv[k][e] * phi[k][e] * r1;
+                gsc[k][e] = fmaf(d[k][e], n1 * wpost[k][e], gsc[k][e]);
+                d[k][e] *= sc[k][e];
+                gpost[k][e] = fmaf(d[k][e], n1, gpost[k][e]);
+                d[k][e] *= wpost[k][e];
+                ss[0] = fmaf(d[k][e], n1, ss[0]);
+            }
+        if (p.post) {
+            sum(ss);
+            const float m = ss[0] * inv;  // mean(s n1)
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) d[k][e] = r1 * fmaf(-(yv[k][e] * phi[k][e] * r1), m, d[k][e]);
+        }
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            float o[kE];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] = d[k][e] * phi[k][e];
+            if (live) store_piece<S, VEC>(p.dy, p.grad_bf16, at, lane, k, p.D, o);
+            if (p.dgate) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) o[e] = d[k][e] * yv[k][e] * dphi[k][e];
+                if (live) store_piece<S, VEC>(p.dgate, p.grad_bf16, at, lane, k, p.D, o);
+            }
+        }
+    }
+    // this workgroup's column sums
+    auto put = [&](float* to, float (&g)[S::K][kE]) {
+        if (S::ROWS == 1) {
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const int c = col_of<S, VEC>(lane, k, e);
+                    if (c < p.D) to[c] = g[k][e];
+                }
+        } else {
+            __syncthreads();
+#pragma unroll
+            for (int e = 0; e < kE; ++e) cols[sub][col_of<S, VEC>(lane, 0, e)] = g[0][e];
+            __syncthreads();
+            for (int c = threadIdx.x; c < p.D; c += S::NT) {
+                float s = 0.0f;
+                for (int i = 0; i < S::ROWS; ++i) s += cols[i][c];
+                to[c] = s;
+            }
+        }
+    };
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.D;
+    if (p.dw_post) put(part, gpost);
+    if (p.dscale) put(part + p.D, gsc);
+    if (p.dw_pre) put(part + 2 * p.D, gpre);
+}
+
+// out[c] = sum over the workgroups of part[g][which][c]: 64 columns and 16 rows of
+// threads to a workgroup, each adding every 16th row in order.
+__global__ __launch_bounds__(1024) void layer_norm_cols_kernel(NormParams p) {
+    __shared__ float s[16][64];
+    const int which = blockIdx.y;
+    float* out = which == 0 ? p.dw_post : which == 1 ? p.dscale : p.dw_pre;
+    if (!out) return;
+    const int l = threadIdx.x & 63, r = threadIdx.x >> 6;
+    const int c = blockIdx.x * 64 + l;
+    float a = 0.0f;
+    if (c < p.D) {
+#pragma unroll 8
+        for (int g = r; g < p.groups; g += 16) a += p.part[(static_cast<int64_t>(g) * 3 + which) * p.D + c];
+    }
+    s[r][l] = a;
+    __syncthreads();
+    if (r == 0 && c < p.D) {
+        float t = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += s[i][l];
+        out[c] = t;
+    }
+}
+
+template <typename TIn, typename TRes>
+void launch(const NormParams& p, hipStream_t st) {
+    with_shape(p.D, [&](auto s) {
+        using S = decltype(s);
+        if (p.vec)
+            hipLaunchKernelGGL((layer_norm_bwd_kernel<S, true, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+        else
+            hipLaunchKernelGGL((layer_norm_bwd_kernel<S, false, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+    });
+}
+
+}  // namespace
+
+int launch_norm_bwd(const NormParams& p, hipStream_t st) {
+    if (p.in_bf16)
+        p.res_bf16 ? launch<uint16_t, uint16_t>(p, st) : launch<uint16_t, float>(p, st);
+    else
+        p.res_bf16 ? launch<float, uint16_t>(p, st) : launch<float, float>(p, st);
+    if (p.dw_post || p.dscale || p.dw_pre)
+        hipLaunchKernelGGL(layer_norm_cols_kernel, dim3((p.D + 63) / 64, 3), dim3(1024), 0, st, p);
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+}  // namespace layer

@@ -1,0 +1,122 @@
+// layer_norm_fwd.hip -- the norm after a block, its gate, the residual and the
+// norm before the next block, in one pass over the rows:
+//     u = y phi(gate),  n = u / rms(u) w_post,  x' = x + scale n,
+//     z = x' / rms(x') w_pre,   rms(a) = sqrt(mean(a^2) + eps).
+// x' leaves rounded to its own type; z is taken from x' before that rounding.
+#include "layer_norm.h"
+
+namespace layer {
+namespace {
+
+template <typename S, bool VEC, typename TIn, typename TRes>
+__global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
+    __shared__ float red[2][S::NT / 64][1];
+    RowSum<S, 1> sum{red};
+    const int lane = threadIdx.x % S::TPR;
+    const int sub = threadIdx.x / S::TPR;
+    const float inv = 1.0f / static_cast<float>(p.D);
+
+    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
+        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
+        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
+    }
+    const int steps = (p.R + S::ROWS - 1) / S::ROWS;
+    for (int it = blockIdx.x; it < steps; it += gridDim.x) {
+        const int row = it * S::ROWS + sub;
+        const bool live = row < p.R;  // past the end: a row of zeros, in step with the barriers
+        const int64_t at = static_cast<int64_t>(row) * p.D;
+        float u[S::K][kE], xo[S::K][kE];
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            Piece<TIn> ry = {}, rg = {};
+            Piece<TRes> rx = {};
+            if (live && p.y) load_piece<S, VEC>(static_cast<const TIn*>(p.y) + at, lane, k, p.D, ry);
+            if (live && p.gate) load_piece<S, VEC>(static_cast<const TIn*>(p.gate) + at, lane, k, p.D, rg);
+            if (live && p.x) load_piece<S, VEC>(static_cast<const TRes*>(p.x) + at, lane, k, p.D, rx);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                u[k][e] = widen(ry.e[e]);
+                xo[k][e] = widen(rx.e[e]);
+            }
+            if (p.gate_kind == 1) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) u[k][e] *= osr::gelu(widen(rg.e[e]));
+            } else if (p.gate_kind == 2) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float g = widen(rg.e[e]);
+                    float s, r;
+                    sigmoid2(g, s, r);
+                    u[k][e] *= g * s;
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kE; ++e) ss[0] = fmaf(u[k][e], u[k][e], ss[0]);
+        }
+        if (p.y) {
+            float r1 = 1.0f;
+            if (p.post) {
+                sum(ss);
+                r1 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+            }
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) xo[k][e] = fmaf(u[k][e] * r1 * wpost[k][e], sc[k][e], xo[k][e]);
+        }
+        if (p.x_out && live) {
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(p.x_out, p.res_bf16, at, lane, k, p.D, xo[k]);
+        }
+        if (p.pre) {
+            ss[0] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) ss[0] = fmaf(xo[k][e], xo[k][e], ss[0]);
+            sum(ss);
+            const float r2 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+#pragma unroll
+                for (int e = 0; e < kE; ++e) xo[k][e] *= r2 * wpre[k][e];
+                if (live) store_piece<S, VEC>(p.z, p.in_bf16, at, lane, k, p.D, xo[k]);
+            }
+        }
+    }
+}
+
+template <typename TIn, typename TRes>
+void launch(const NormParams& p, hipStream_t st) {
+    with_shape(p.D, [&](auto s) {
+        using S = decltype(s);
+        if (p.vec)
+            hipLaunchKernelGGL((layer_norm_fwd_kernel<S, true, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+        else
+            hipLaunchKernelGGL((layer_norm_fwd_kernel<S, false, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+    });
+}
+
+}  // namespace
+
+int norm_groups(int R, int D, bool backward) {
+    int rows = 1, nt = 256;
+    with_shape(D, [&](auto s) { rows = decltype(s)::ROWS, nt = decltype(s)::NT; });
+    const int steps = (R + rows - 1) / rows;
+    const int most = (backward ? 512 : 1024) * 256 / nt;
+    return steps < most ? steps : most;
+}
+
+int launch_norm_fwd(const NormParams& p, hipStream_t st) {
+    if (p.in_bf16)
+        p.res_bf16 ? launch<uint16_t, uint16_t>(p, st) : launch<uint16_t, float>(p, st);
+    else
+        p.res_bf16 ? launch<float, uint16_t>(p, st) : launch<float, float>(p, st);
+    return hipGetLastError() == hipSuccess ? 0 : -5;
+}
+
+}  // namespace layer

@@ -25,6 +25,8 @@ PAIRS_AUTO, PAIRS_OFF = 0, 1
 WGS_AUTO, WGS_ONE = 0, 1
 OVERLAP_AUTO, OVERLAP_OFF = 0, 1
 BWD_AUTO, BWD_WALK, BWD_CHUNK = 0, 1, 2
+SCAN_ONE, SCAN_COMPLEMENT, SCAN_NORM = 0, 1, 2
+GATE_NONE, GATE_GELU, GATE_SILU = 0, 1, 2
 
 OK = 0
 ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_LAUNCH, ERR_ALIAS, ERR_ALIGN = -1, -2, -3, -4, -5, -6, -7
@@ -33,7 +35,10 @@ EXPORTED = ("lattice_osr_fwd_chunked", "lattice_osr_fwd_recurrent", "lattice_osr
             "lattice_osr_workspace_bytes", "lattice_osr_status_string", "lattice_osr_abi_version",
             "lattice_osr_bwd_chunked", "lattice_osr_bwd_workspace_bytes", "lattice_osr_glue_pre",
             "lattice_osr_glue_post", "lattice_osr_fwd_chunked_gated", "lattice_osr_fwd_chunked_noalloc",
-            "lattice_osr_fwd_chunked_save", "lattice_osr_bwd_chunked_saved")
+            "lattice_osr_fwd_chunked_save", "lattice_osr_bwd_chunked_saved", "lattice_osr_scan_fwd",
+            "lattice_osr_scan_bwd", "lattice_osr_scan_step", "lattice_osr_scan_saved_bytes",
+            "lattice_osr_scan_workspace_bytes", "lattice_osr_norm_fwd", "lattice_osr_norm_bwd",
+            "lattice_osr_norm_bwd_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -41,6 +46,16 @@ class lattice_osr_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("B", "T", "H", "m", "d", "gamma_per_slot", "in_dtype", "y_dtype", "mode", "linearisation",
                  "schedule", "chain_pairs", "chain_wgs", "readout_overlap", "bwd_form")]
+
+
+class lattice_osr_scan_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "in_dtype", "y_dtype", "grad_dtype", "input_weight")]
+
+
+class lattice_osr_norm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("R", "D", "in_dtype", "res_dtype", "grad_dtype", "gate_kind", "post_norm", "pre_norm")] + \
+               [("eps", ctypes.c_float)]
 
 
 class OSRError(RuntimeError):
@@ -85,6 +100,17 @@ def load_library():
         lib.lattice_osr_glue_pre.restype = ctypes.c_int
         lib.lattice_osr_glue_post.argtypes = [dp, vp, vp, vp, vp]
         lib.lattice_osr_glue_post.restype = ctypes.c_int
+        sp, np_, sz = ctypes.POINTER(lattice_osr_scan_desc), ctypes.POINTER(lattice_osr_norm_desc), ctypes.c_size_t
+        lib.lattice_osr_scan_fwd.argtypes = [sp] + [vp] * 8 + [sz, vp, sz, vp]
+        lib.lattice_osr_scan_bwd.argtypes = [sp] + [vp] * 5 + [sz] + [vp] * 7 + [sz, vp]
+        lib.lattice_osr_scan_step.argtypes = [sp] + [vp] * 7
+        lib.lattice_osr_norm_fwd.argtypes = [np_] + [vp] * 9
+        lib.lattice_osr_norm_bwd.argtypes = [np_] + [vp] * 15 + [sz, vp]
+        for f in ("scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd"):
+            getattr(lib, "lattice_osr_" + f).restype = ctypes.c_int
+        for f, d in (("scan_saved_bytes", sp), ("scan_workspace_bytes", sp), ("norm_bwd_workspace_bytes", np_)):
+            getattr(lib, "lattice_osr_" + f).argtypes = [d]
+            getattr(lib, "lattice_osr_" + f).restype = sz
         lib.lattice_osr_status_string.argtypes = [ctypes.c_int]
         lib.lattice_osr_status_string.restype = ctypes.c_char_p
         lib.lattice_osr_abi_version.argtypes = []
@@ -495,6 +521,301 @@ def lattice_osr_glue_post(y, gate, *, out=None, stream=None):
     if rc != OK:
         raise OSRError(rc, "lattice_osr_glue_post")
     return out
+
+
+# ---------------------------------------- element-wise gated recurrence --
+def _on(device, stream, fn):
+    """fn(stream handle) with the tensors' device current and, where a stream
+    is given, under it, so that what fn allocates follows its order."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return fn(torch.cuda.current_stream().cuda_stream)
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, expected {device}")
+    with torch.cuda.device(device):
+        st = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(st):
+            return fn(st.cuda_stream)
+
+
+def _bytes_of(fn, desc):
+    n = int(getattr(load_library(), fn)(ctypes.byref(desc)))
+    if n == ctypes.c_size_t(-1).value:
+        raise OSRError(ERR_SHAPE, fn)
+    return n
+
+
+def make_scan_desc(B, T, D, in_dtype=BF16, y_dtype=F32, grad_dtype=F32, input_weight=SCAN_COMPLEMENT):
+    return lattice_osr_scan_desc(B, T, D, in_dtype, y_dtype, grad_dtype, input_weight)
+
+
+def lattice_osr_scan_saved_bytes(desc: lattice_osr_scan_desc) -> int:
+    return _bytes_of("lattice_osr_scan_saved_bytes", desc)
+
+
+def lattice_osr_scan_workspace_bytes(desc: lattice_osr_scan_desc) -> int:
+    return _bytes_of("lattice_osr_scan_workspace_bytes", desc)
+
+
+def _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, grad_dtype, input_weight):
+    """Descriptor of a scan call, after checking every input against it: v,
+    mu_logit, gamma_logit [B,T,D] or [B,T,H,d] in one dtype, lengths [B] int32;
+    all contiguous, on one GPU.  Returns it with the states' shape."""
+    if v.dim() not in (3, 4):
+        raise ValueError("v/mu_logit/gamma_logit are [B,T,D] or [B,T,H,d]")
+    if v.dtype not in _DT:
+        raise ValueError("inputs must be float32 or bfloat16")
+    if y_dtype not in _DT or grad_dtype not in _DT:
+        raise ValueError("y_dtype and grad_dtype must be torch.float32 or torch.bfloat16")
+    shape, dev = v.shape, v.device
+    _check_tensor("v", v, shape, None)
+    _check_tensor("mu_logit", mu_logit, shape, v.dtype, dev)
+    if gamma_logit is not None:
+        _check_tensor("gamma_logit", gamma_logit, shape, v.dtype, dev)
+    if lengths is not None:
+        _check_tensor("lengths", lengths, (shape[0],), torch.int32, dev)
+    D = shape[2] if len(shape) == 3 else shape[2] * shape[3]
+    if max(shape[0], shape[1], D) > 2 ** 31 - 1:
+        raise ValueError(f"shape {tuple(shape)}: sizes are at most 2^31 - 1")
+    desc = lattice_osr_scan_desc(shape[0], shape[1], D, _DT[v.dtype], _DT[y_dtype], _DT[grad_dtype], input_weight)
+    return desc, (shape[0], *shape[2:])
+
+
+def _scan_workspace(desc, workspace, device):
+    return _workspace(workspace, lattice_osr_scan_workspace_bytes(desc), device)
+
+
+def lattice_osr_scan_fwd(v, mu_logit, state_in=None, *, gamma_logit=None, lengths=None,
+                         input_weight: int = SCAN_COMPLEMENT, y_dtype=torch.float32, y=None, state_out=None,
+                         save: bool = False, saved=None, workspace=None, stream=None):
+    """h_t = mu_t h_{t-1} + w(mu_t) gamma_t v_t with mu = sigmoid(mu_logit) and
+    gamma = sigmoid(gamma_logit) (1 without it), y = h; w by input_weight: 1,
+    1 - mu or sqrt(1 - mu^2).
+
+    v, mu_logit, gamma_logit [B,T,D] or [B,T,H,d] share a dtype (float32 or bfloat16);
+    state_in (None: zeros) and state_out are [B,D] or [B,H,d] float32, state_out may
+    be state_in; lengths [B] int32: the tokens of each sequence, y is zero behind them.
+    Returns (y, state_out) and, with save (or `saved`, a uint8 tensor of
+    lattice_osr_scan_saved_bytes), what lattice_osr_scan_bwd needs."""
+    lib = load_library()
+    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, torch.float32, input_weight)
+    dev = v.device
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            _check_tensor(name, t, sshape, torch.float32, dev)
+    if y is not None:
+        _check_tensor("y", y, v.shape, y_dtype, dev)
+    _check_cuda(v)
+    save = save or saved is not None
+
+    def call(st):
+        yy = torch.empty(v.shape, dtype=y_dtype, device=dev) if y is None else y
+        so = torch.empty(sshape, dtype=torch.float32, device=dev) if state_out is None else state_out
+        sv, sbytes = _workspace(saved, lattice_osr_scan_saved_bytes(desc), dev) if save else (None, 0)
+        ws, wbytes = _scan_workspace(desc, workspace, dev)
+        rc = lib.lattice_osr_scan_fwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
+                                      _ptr(state_in), _ptr(so), _ptr(yy), _ptr(sv), sbytes, _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_scan_fwd")
+        return (yy, so, sv) if save else (yy, so)
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_scan_bwd(v, mu_logit, dy, dstate_out=None, *, saved, gamma_logit=None, lengths=None,
+                         input_weight: int = SCAN_COMPLEMENT, grad_dtype=torch.float32, grads: Optional[dict] = None,
+                         workspace=None, stream=None) -> dict:
+    """Gradients of sum(dy*y) + sum(dstate_out*state_out) of lattice_osr_scan_fwd with
+    the same inputs, whose `saved` this call takes.  dy has v's shape (float32 or
+    bfloat16), dstate_out the state's (None: zeros).  Returns a dict of dv, dmu_logit
+    (and dgamma_logit, with gamma_logit) in grad_dtype and dstate_in in float32,
+    allocated unless passed in `grads`."""
+    lib = load_library()
+    if saved is None:
+        raise ValueError("saved: the tensor lattice_osr_scan_fwd returned with save=True")
+    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, dy.dtype, grad_dtype, input_weight)
+    dev = v.device
+    _check_tensor("dy", dy, v.shape, None, dev)
+    if dstate_out is not None:
+        _check_tensor("dstate_out", dstate_out, sshape, torch.float32, dev)
+    want = [("dv", v.shape, grad_dtype), ("dmu_logit", v.shape, grad_dtype)]
+    if gamma_logit is not None:
+        want.append(("dgamma_logit", v.shape, grad_dtype))
+    want.append(("dstate_in", sshape, torch.float32))
+    _check_grads(grads, want, dev)
+    _check_cuda(v)
+
+    def call(st):
+        g = _grads(grads, want, dev)
+        sv, sbytes = _workspace(saved, 0, dev)
+        ws, wbytes = _scan_workspace(desc, workspace, dev)
+        rc = lib.lattice_osr_scan_bwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
+                                      _ptr(sv), sbytes, _ptr(dy), _ptr(dstate_out), _ptr(g["dv"]),
+                                      _ptr(g["dmu_logit"]), _ptr(g.get("dgamma_logit")), _ptr(g["dstate_in"]),
+                                      _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_scan_bwd")
+        return g
+
+    return _on(dev, stream, call)
+
+
+def _check_grads(grads, want, dev):
+    if grads is None:
+        return
+    for name, shape, dtype in want:
+        if name not in grads:
+            raise ValueError(f"grads lacks {name}")
+        _check_tensor(name, grads[name], shape, dtype, dev)
+
+
+def _grads(grads, want, dev):
+    if grads is not None:
+        return {name: grads[name] for name, _, _ in want}
+    return {name: torch.empty(shape, dtype=dtype, device=dev) for name, shape, dtype in want}
+
+
+def lattice_osr_scan_step(v, mu_logit, state_in, *, gamma_logit=None, input_weight: int = SCAN_COMPLEMENT,
+                          y_dtype=torch.float32, y=None, state_out=None, stream=None):
+    """One token of lattice_osr_scan_fwd (T = 1) for every sequence; state_out
+    may be state_in (in place).  Returns (y, state_out)."""
+    lib = load_library()
+    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, None, y_dtype, torch.float32, input_weight)
+    dev = v.device
+    _check_tensor("state_in", state_in, sshape, torch.float32, dev)
+    if state_out is not None:
+        _check_tensor("state_out", state_out, sshape, torch.float32, dev)
+    if y is not None:
+        _check_tensor("y", y, v.shape, y_dtype, dev)
+    _check_cuda(v)
+
+    def call(st):
+        yy = torch.empty(v.shape, dtype=y_dtype, device=dev) if y is None else y
+        so = torch.empty_like(state_in) if state_out is None else state_out
+        rc = lib.lattice_osr_scan_step(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit),
+                                       _ptr(state_in), _ptr(so), _ptr(yy), st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_scan_step")
+        return yy, so
+
+    return _on(dev, stream, call)
+
+
+# ------------------------------------------------- norms around a block --
+def make_norm_desc(R, D, in_dtype=BF16, res_dtype=BF16, grad_dtype=F32, gate_kind=GATE_NONE, post_norm=1, pre_norm=1,
+                   eps=1e-6):
+    return lattice_osr_norm_desc(R, D, in_dtype, res_dtype, grad_dtype, gate_kind, post_norm, pre_norm, eps)
+
+
+def lattice_osr_norm_bwd_workspace_bytes(desc: lattice_osr_norm_desc) -> int:
+    return _bytes_of("lattice_osr_norm_bwd_workspace_bytes", desc)
+
+
+def _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre, eps, z_dtype, x_dtype, grad_dtype):
+    """Descriptor of a norm call, after checking every input against it: rows
+    [..., D] of y, gate (one dtype) and x, weights [D] float32; all contiguous,
+    on one GPU."""
+    lead = y if y is not None else x
+    if lead is None:
+        raise ValueError("pass y, x or both")
+    if lead.dim() < 1:
+        raise ValueError("y, x and gate are [..., D]")
+    shape, dev = lead.shape, lead.device
+    D = shape[-1]
+    in_dtype = y.dtype if y is not None else z_dtype or x.dtype
+    res_dtype = x.dtype if x is not None else x_dtype or in_dtype
+    for dt in (in_dtype, res_dtype, grad_dtype):
+        if dt not in _DT:
+            raise ValueError("tensors must be float32 or bfloat16")
+    if gate is None:
+        gate_kind = GATE_NONE
+    elif gate_kind == GATE_NONE:
+        raise ValueError("gate given with GATE_NONE")
+    for name, t, dt in (("y", y, in_dtype), ("x", x, res_dtype), ("gate", gate, in_dtype)):
+        if t is not None:
+            _check_tensor(name, t, shape, dt, dev)
+    for name, t in (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)):
+        if t is not None:
+            _check_tensor(name, t, (D,), torch.float32, dev)
+    R = lead.numel() // D if D else 0
+    if R > 2 ** 31 - 1:
+        raise ValueError(f"{R} rows: at most 2^31 - 1")
+    desc = lattice_osr_norm_desc(R, D, _DT[in_dtype], _DT[res_dtype], _DT[grad_dtype],
+                                 gate_kind, int(post_norm and y is not None), int(pre_norm), eps)
+    return desc, lead, in_dtype, res_dtype
+
+
+def lattice_osr_norm_fwd(y=None, x=None, *, gate=None, gate_kind: int = GATE_GELU, post_norm: bool = True,
+                         w_post=None, scale=None, pre_norm: bool = True, w_pre=None, eps: float = 1e-6,
+                         z_dtype=None, x_dtype=None, x_out=None, z=None, stream=None):
+    """u = y phi(gate), n = u / rms(u) w_post, x_out = x + scale n, z = x_out / rms(x_out) w_pre
+    over the last dimension, rms(a) = sqrt(mean(a^2) + eps).
+
+    y and gate [..., D] share a dtype, which is z's too; x [..., D] has its own (float32 or
+    bfloat16 each); the weights are [D] float32, None: ones.  gate None: no gate; gate_kind
+    GATE_GELU or GATE_SILU.  x None: no residual, x_out in x_dtype (y's dtype if None).  y None:
+    only z = x / rms(x) w_pre, in z_dtype (x's dtype if None).  x_out may be x (in place).
+    Returns (x_out, z); x_out is None without y, z without pre_norm."""
+    lib = load_library()
+    desc, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
+                                                 eps, z_dtype, x_dtype, torch.float32)
+    dev = lead.device
+    if z_dtype is not None and z_dtype != in_dtype:
+        raise ValueError("z_dtype is y's dtype")
+    if x_dtype is not None and x_dtype != res_dtype:
+        raise ValueError("x_dtype is x's dtype")
+    if x_out is not None:
+        _check_tensor("x_out", x_out, lead.shape, res_dtype, dev)
+    if z is not None:
+        _check_tensor("z", z, lead.shape, in_dtype, dev)
+    _check_cuda(lead)
+
+    def call(st):
+        xo = torch.empty(lead.shape, dtype=res_dtype, device=dev) if x_out is None and y is not None else x_out
+        zz = torch.empty(lead.shape, dtype=in_dtype, device=dev) if z is None and pre_norm else z
+        rc = lib.lattice_osr_norm_fwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
+                                      _ptr(w_pre), _ptr(xo), _ptr(zz), st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_norm_fwd")
+        return xo, zz
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_norm_bwd(y=None, x=None, dx_out=None, dz=None, *, gate=None, gate_kind: int = GATE_GELU,
+                         post_norm: bool = True, w_post=None, scale=None, pre_norm: bool = True, w_pre=None,
+                         eps: float = 1e-6, grad_dtype=torch.float32, grads: Optional[dict] = None, workspace=None,
+                         stream=None) -> dict:
+    """Gradients of sum(dx_out*x_out) + sum(dz*z) of lattice_osr_norm_fwd with the same inputs.
+    dx_out (x's dtype; None with pre_norm: zeros) and dz (y's dtype, with pre_norm) have y's shape.
+    Returns a dict of dy, dgate (grad_dtype), dx (x's dtype) and dw_post, dscale, dw_pre (float32), each
+    where its operand was passed, allocated unless passed in `grads` (dx may be dx_out)."""
+    lib = load_library()
+    desc, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
+                                                 eps, dz.dtype if dz is not None else None,
+                                                 dx_out.dtype if dx_out is not None else None, grad_dtype)
+    dev = lead.device
+    for name, t, dt in (("dx_out", dx_out, res_dtype), ("dz", dz, in_dtype)):
+        if t is not None:
+            _check_tensor(name, t, lead.shape, dt, dev)
+    want = [(n, t.shape, dt) for n, t, dt in (("dy", y, grad_dtype), ("dgate", gate, grad_dtype), ("dx", x, res_dtype),
+                                              ("dw_post", w_post, torch.float32), ("dscale", scale, torch.float32),
+                                              ("dw_pre", w_pre, torch.float32)) if t is not None]
+    _check_grads(grads, want, dev)
+    _check_cuda(lead)
+
+    def call(st):
+        g = _grads(grads, want, dev)
+        sums = w_post is not None or scale is not None or w_pre is not None
+        ws, wbytes = _workspace(workspace, lattice_osr_norm_bwd_workspace_bytes(desc) if sums else 0, dev)
+        rc = lib.lattice_osr_norm_bwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
+                                      _ptr(w_pre), _ptr(dx_out), _ptr(dz), _ptr(g.get("dy")), _ptr(g.get("dgate")),
+                                      _ptr(g.get("dx")), _ptr(g.get("dw_post")), _ptr(g.get("dscale")),
+                                      _ptr(g.get("dw_pre")), _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_norm_bwd")
+        return g
+
+    return _on(dev, stream, call)
 
 
 def to_device(inp, device="cuda") -> dict:

@@ -416,6 +416,142 @@ LATTICE_OSR_API int lattice_osr_glue_pre(const lattice_osr_desc* desc, const voi
 LATTICE_OSR_API int lattice_osr_glue_post(const lattice_osr_desc* desc, const void* y, const void* gate, void* out,
                                           void* hip_stream);
 
+/*
+ * Element-wise gated recurrence (scan): per channel and token, with
+ *   mu = sigmoid(mu_logit),  gamma = sigmoid(gamma_logit) (1 where it is NULL),
+ *   h_t = mu_t h_{t-1} + w(mu_t) gamma_t v_t,   y_t = h_t,
+ * the diagonal counterpart of the OSR's forget gate mu and writing intensity
+ * gamma, for layers that mix both kinds of state.  h_{-1} is state_in (zeros
+ * where it is NULL).  Arithmetic, gates and states are fp32.
+ *   v, mu_logit, gamma_logit  [B, T, D]  in_dtype   (D = heads x width)
+ *   y                         [B, T, D]  y_dtype
+ *   state_in, state_out       [B, D]     float32
+ *   lengths                   [B]        int32, or NULL (every sequence has T
+ *                             tokens): tokens from lengths[b] on are padding,
+ *                             whatever their values; y is written as zeros
+ *                             there and state_out is the state after the last
+ *                             token (state_in where there is none).  Values
+ *                             outside [0, T] are taken as the nearer end.
+ * mu_logit = -inf drops the state before a token (a document's border inside a
+ * row), +inf keeps it; either has a zero gradient.  D up to 2^20 and T up
+ * to 2^30, odd ones included; element alignment only (rows move in wider pieces
+ * where D and the addresses allow).  B ceil(D / 64) must stay below 2^22.
+ */
+#define LATTICE_OSR_SCAN_ONE 0        /* w = 1                  */
+#define LATTICE_OSR_SCAN_COMPLEMENT 1 /* w = 1 - mu             */
+#define LATTICE_OSR_SCAN_NORM 2       /* w = sqrt(1 - mu^2)     */
+
+typedef struct {
+    int32_t B;            /* sequences                                      */
+    int32_t T;            /* tokens per sequence                            */
+    int32_t D;            /* channels                                       */
+    int32_t in_dtype;     /* LATTICE_OSR_F32 or LATTICE_OSR_BF16            */
+    int32_t y_dtype;      /* of y and dy                                    */
+    int32_t grad_dtype;   /* of dv, dmu_logit and dgamma_logit              */
+    int32_t input_weight; /* LATTICE_OSR_SCAN_ONE, _COMPLEMENT or _NORM     */
+} lattice_osr_scan_desc;
+
+/*
+ * Forward.  state_out may be NULL (not wanted) or state_in itself; no other
+ * output may overlap an argument (ERR_ALIAS).  saved, where not NULL, receives
+ * what lattice_osr_scan_bwd needs (lattice_osr_scan_saved_bytes(desc) bytes, 4-byte
+ * aligned).  workspace must hold lattice_osr_scan_workspace_bytes(desc) bytes
+ * (NULL allowed where that is 0); its contents on entry are ignored, and calls
+ * that may overlap in time need one each.  Results do not depend on how the
+ * work is split: reruns agree bit for bit.  Errors and asynchrony as above.
+ */
+LATTICE_OSR_API int lattice_osr_scan_fwd(const lattice_osr_scan_desc* desc, const void* v, const void* mu_logit,
+                                         const void* gamma_logit, const int32_t* lengths, const float* state_in,
+                                         float* state_out, void* y, void* saved, size_t saved_bytes, void* workspace,
+                                         size_t workspace_bytes, void* hip_stream);
+
+/*
+ * Backward: the gradient of L = sum(dy * y) + sum(dstate_out * state_out),
+ * with the forward's inputs, descriptor and `saved` (unchanged since).
+ *   dy  [B, T, D] y_dtype;  dstate_out [B, D] float32, or NULL (zeros)
+ *   dv, dmu_logit, dgamma_logit  [B, T, D]  grad_dtype (dgamma_logit NULL
+ *                                exactly where gamma_logit is)
+ *   dstate_in  [B, D] float32, or NULL (not wanted)
+ * Every gradient is written in full, zeros at padding; no output may overlap
+ * an argument.  The workspace is the forward's size.
+ */
+LATTICE_OSR_API int lattice_osr_scan_bwd(const lattice_osr_scan_desc* desc, const void* v, const void* mu_logit,
+                                         const void* gamma_logit, const int32_t* lengths, const void* saved,
+                                         size_t saved_bytes, const void* dy, const float* dstate_out, void* dv,
+                                         void* dmu_logit, void* dgamma_logit, float* dstate_in, void* workspace,
+                                         size_t workspace_bytes, void* hip_stream);
+
+/* One token for each of B sequences (desc->T must be 1): y = state_out = h.
+ * state_out may be state_in (in place).  No lengths, no workspace. */
+LATTICE_OSR_API int lattice_osr_scan_step(const lattice_osr_scan_desc* desc, const void* v, const void* mu_logit,
+                                          const void* gamma_logit, const float* state_in, float* state_out, void* y,
+                                          void* hip_stream);
+
+/* Bytes of `saved` and of the workspace; (size_t)-1 for an invalid descriptor. */
+LATTICE_OSR_API size_t lattice_osr_scan_saved_bytes(const lattice_osr_scan_desc* desc);
+LATTICE_OSR_API size_t lattice_osr_scan_workspace_bytes(const lattice_osr_scan_desc* desc);
+
+/*
+ * Norms around a block, fused with the block's gate and residual: over rows of
+ * D values, with rms(a) = sqrt(mean(a^2) + eps),
+ *   u = y phi(gate),   n = u / rms(u) w_post      (post_norm; else n = u),
+ *   x' = x + scale n,  z = x' / rms(x') w_pre     (pre_norm).
+ * phi is 1, GeLU in its exact form (the layer's post-gate) or SiLU; a weight or
+ * scale that is NULL is 1 throughout, an x that is NULL is 0.  y NULL with
+ * neither gate, post_norm nor scale: the norm before a first block, x' = x.
+ * z is taken from x' in fp32, before x_out is rounded to its type.
+ *   y, gate, z           [R, D]  in_dtype
+ *   x, x_out             [R, D]  res_dtype
+ *   w_post, scale, w_pre [D]     float32
+ * D is at most 16384; element alignment (16-byte aligned rows with D a multiple
+ * of 8 move in wider pieces).  eps must be a normal positive number.
+ */
+#define LATTICE_OSR_GATE_NONE 0
+#define LATTICE_OSR_GATE_GELU 1
+#define LATTICE_OSR_GATE_SILU 2
+
+typedef struct {
+    int32_t R;          /* rows (tokens, or tokens x heads)               */
+    int32_t D;          /* values per row                                 */
+    int32_t in_dtype;   /* of y, gate, z and dz                           */
+    int32_t res_dtype;  /* of x, x_out, dx_out and dx                     */
+    int32_t grad_dtype; /* of dy and dgate                                */
+    int32_t gate_kind;  /* LATTICE_OSR_GATE_NONE (gate NULL), _GELU, _SILU */
+    int32_t post_norm;  /* 1: the norm of the block's output              */
+    int32_t pre_norm;   /* 1: the norm before the next block, z           */
+    float eps;
+} lattice_osr_norm_desc;
+
+/*
+ * Forward.  x_out may be NULL with pre_norm (only z wanted; it must be where y
+ * is NULL) and may be x itself; z is NULL exactly without pre_norm.  No other
+ * overlap of an output (ERR_ALIAS).  A missing operand is ERR_NULL, one that
+ * the descriptor has no use for ERR_UNSUPPORTED.
+ */
+LATTICE_OSR_API int lattice_osr_norm_fwd(const lattice_osr_norm_desc* desc, const void* y, const void* gate,
+                                         const void* x, const float* w_post, const float* scale, const float* w_pre,
+                                         void* x_out, void* z, void* hip_stream);
+
+/*
+ * Backward: the gradient of L = sum(dx_out * x') + sum(dz * z), with the
+ * forward's inputs (its outputs are not needed; the forward must not have run
+ * in place on x).
+ *   dx_out  [R, D] res_dtype, or NULL with pre_norm (zeros)
+ *   dz      [R, D] in_dtype, exactly with pre_norm
+ *   dy, dgate  [R, D] grad_dtype, exactly where y, gate are
+ *   dx      [R, D] res_dtype; NULL without x, or where it is not wanted; may be dx_out itself
+ *   dw_post, dscale, dw_pre  [D] float32, each NULL where it is not wanted
+ * workspace: lattice_osr_norm_bwd_workspace_bytes(desc) bytes, 4-byte aligned (NULL
+ * allowed without the last three).  The sums over rows are taken in a fixed
+ * order: reruns agree bit for bit.
+ */
+LATTICE_OSR_API int lattice_osr_norm_bwd(const lattice_osr_norm_desc* desc, const void* y, const void* gate,
+                                         const void* x, const float* w_post, const float* scale, const float* w_pre,
+                                         const void* dx_out, const void* dz, void* dy, void* dgate, void* dx,
+                                         float* dw_post, float* dscale, float* dw_pre, void* workspace,
+                                         size_t workspace_bytes, void* hip_stream);
+LATTICE_OSR_API size_t lattice_osr_norm_bwd_workspace_bytes(const lattice_osr_norm_desc* desc);
+
 /* Static text for a status code (never NULL). */
 LATTICE_OSR_API const char* lattice_osr_status_string(int status);
 
