@@ -41,8 +41,9 @@ int check_scan(const lattice_osr_scan_desc* d) {
     if (d->B <= 0 || d->T <= 0 || d->D <= 0) return LATTICE_OSR_ERR_SHAPE;
     if (d->T > (1 << 30) || d->D > (1 << 20)) return LATTICE_OSR_ERR_SHAPE;
     if (static_cast<int64_t>(d->B) * d->T > (INT64_C(1) << 40) / d->D) return LATTICE_OSR_ERR_SHAPE;
-    // a launch has fewer than 2^32 threads: at most 1024 for each 64 channels of a sequence
-    if ((static_cast<int64_t>(d->D) + 63) / 64 * d->B > (INT64_C(1) << 22) - 1) return LATTICE_OSR_ERR_SHAPE;
+    // a launch has fewer than 2^32 threads: at most 1024 for each tile of 64 channels
+    const int64_t tiles = layer::tiles_of(d->T, layer::kBwdTile);
+    if ((static_cast<int64_t>(d->D) + 63) / 64 * d->B >= (INT64_C(1) << 22) / tiles) return LATTICE_OSR_ERR_SHAPE;
     if (!dtype_ok(d->in_dtype) || !dtype_ok(d->y_dtype) || !dtype_ok(d->grad_dtype)) return LATTICE_OSR_ERR_UNSUPPORTED;
     if (d->input_weight < LATTICE_OSR_SCAN_ONE || d->input_weight > LATTICE_OSR_SCAN_NORM)
         return LATTICE_OSR_ERR_UNSUPPORTED;
@@ -50,8 +51,7 @@ int check_scan(const lattice_osr_scan_desc* d) {
 }
 
 size_t scan_saved_bytes(const lattice_osr_scan_desc* d) {
-    const size_t tiles = (static_cast<size_t>(d->T) + layer::kScanTile - 1) / layer::kScanTile;
-    return static_cast<size_t>(d->B) * tiles * d->D * sizeof(float);
+    return static_cast<size_t>(d->B) * layer::tiles_of(d->T, layer::kBwdTile) * d->D * sizeof(float);
 }
 
 layer::ScanParams scan_params(const lattice_osr_scan_desc* d) {
@@ -119,7 +119,8 @@ size_t lattice_osr_scan_saved_bytes(const lattice_osr_scan_desc* desc) {
 }
 
 size_t lattice_osr_scan_workspace_bytes(const lattice_osr_scan_desc* desc) {
-    return check_scan(desc) != LATTICE_OSR_OK ? static_cast<size_t>(-1) : 0;
+    if (check_scan(desc) != LATTICE_OSR_OK) return static_cast<size_t>(-1);
+    return layer::scan_workspace_bytes(desc->B, desc->T, desc->D);
 }
 
 int lattice_osr_scan_fwd(const lattice_osr_scan_desc* desc, const void* v, const void* mu_logit,
@@ -130,6 +131,9 @@ int lattice_osr_scan_fwd(const lattice_osr_scan_desc* desc, const void* v, const
     if (rc != LATTICE_OSR_OK) return rc;
     if (!v || !mu_logit || !y) return LATTICE_OSR_ERR_NULL;
     if (saved && saved_bytes < scan_saved_bytes(desc)) return LATTICE_OSR_ERR_WORKSPACE;
+    const size_t need = layer::scan_workspace_bytes(desc->B, desc->T, desc->D);
+    if (need && !workspace) return LATTICE_OSR_ERR_NULL;
+    if (workspace_bytes < need) return LATTICE_OSR_ERR_WORKSPACE;
     const size_t n = static_cast<size_t>(desc->B) * desc->T * desc->D, nb = static_cast<size_t>(desc->B) * desc->D;
     const size_t ei = elem(desc->in_dtype), ey = elem(desc->y_dtype);
     const Buf bufs[] = {{v, n * ei, ei, false},
@@ -139,13 +143,14 @@ int lattice_osr_scan_fwd(const lattice_osr_scan_desc* desc, const void* v, const
                         {state_in == state_out ? nullptr : state_in, nb * 4, 4, false},
                         {state_out, nb * 4, 4, true},
                         {y, n * ey, ey, true},
-                        {saved, scan_saved_bytes(desc), 4, true}};
+                        {saved, scan_saved_bytes(desc), 4, true},
+                        {need ? workspace : nullptr, need, 8, true}};
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
-    (void)workspace, (void)workspace_bytes;
     layer::ScanParams p = scan_params(desc);
     p.v = v, p.f = mu_logit, p.g = gamma_logit, p.lengths = lengths;
     p.state_in = state_in, p.state_out = state_out, p.y = y, p.saved = static_cast<float*>(saved);
+    p.ws = need ? workspace : nullptr, p.group = layer::scan_group(desc->B, desc->T, desc->D);
     return layer::launch_scan_fwd(p, static_cast<hipStream_t>(hip_stream));
 }
 
@@ -159,6 +164,9 @@ int lattice_osr_scan_bwd(const lattice_osr_scan_desc* desc, const void* v, const
     if (gamma_logit && !dgamma_logit) return LATTICE_OSR_ERR_NULL;
     if (!gamma_logit && dgamma_logit) return LATTICE_OSR_ERR_UNSUPPORTED;
     if (saved_bytes < scan_saved_bytes(desc)) return LATTICE_OSR_ERR_WORKSPACE;
+    const size_t need = layer::scan_workspace_bytes(desc->B, desc->T, desc->D);
+    if (need && !workspace) return LATTICE_OSR_ERR_NULL;
+    if (workspace_bytes < need) return LATTICE_OSR_ERR_WORKSPACE;
     const size_t n = static_cast<size_t>(desc->B) * desc->T * desc->D, nb = static_cast<size_t>(desc->B) * desc->D;
     const size_t ei = elem(desc->in_dtype), ey = elem(desc->y_dtype), eg = elem(desc->grad_dtype);
     const Buf bufs[] = {{v, n * ei, ei, false},
@@ -171,14 +179,15 @@ int lattice_osr_scan_bwd(const lattice_osr_scan_desc* desc, const void* v, const
                         {dv, n * eg, eg, true},
                         {dmu_logit, n * eg, eg, true},
                         {dgamma_logit, n * eg, eg, true},
-                        {dstate_in, nb * 4, 4, true}};
+                        {dstate_in, nb * 4, 4, true},
+                        {need ? workspace : nullptr, need, 8, true}};
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
-    (void)workspace, (void)workspace_bytes;
     layer::ScanParams p = scan_params(desc);
     p.v = v, p.f = mu_logit, p.g = gamma_logit, p.lengths = lengths;
     p.saved = const_cast<float*>(static_cast<const float*>(saved));
     p.dy = dy, p.dstate_out = dstate_out;
+    p.ws = need ? workspace : nullptr, p.group = layer::scan_group(desc->B, desc->T, desc->D);
     p.dv = dv, p.df = dmu_logit, p.dg = dgamma_logit, p.dstate_in = dstate_in;
     return layer::launch_scan_bwd(p, static_cast<hipStream_t>(hip_stream));
 }

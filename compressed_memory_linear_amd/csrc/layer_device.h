@@ -56,4 +56,12 @@ __device__ __forceinline__ void sigmoid2(float x, float& s, float& r) {
     r = e > 33554432.0f ? 1.0f : e * s;
 }
 
+// The scan's input weight w(mu), from mu and 1 - mu.
+template <int WT>
+__device__ __forceinline__ float weight_of(float m, float om) {
+    if constexpr (WT == 1) return om;
+    if constexpr (WT == 2) return __builtin_amdgcn_sqrtf(om * (1.0f + m));
+    return 1.0f;
+}
+
 }  // namespace layer

@@ -10,9 +10,11 @@
 
 namespace layer {
 
-// Tokens per tile of the scan: the unit a workgroup loads at once, and the
-// spacing of the states a saving forward keeps for the backward.
-constexpr int kScanTile = 128;
+// Tokens per tile (what a workgroup takes) of the scan's forward and backward.  A saving
+// forward keeps the state before each of the backward's tiles.
+constexpr int kFwdTile = 128;
+constexpr int kBwdTile = 64;
+inline int64_t tiles_of(int64_t T, int tile) { return (T + tile - 1) / tile; }
 
 // Parameters of the scan's kernels; layouts as in include/lattice_osr.h.
 struct ScanParams {
@@ -21,7 +23,7 @@ struct ScanParams {
     const float* state_in;    // [B,D] or null (zeros)
     float* state_out;         // [B,D] or null
     void* y;                  // [B,T,D] (forward)
-    float* saved;             // [B, ceil(T / kScanTile), D]: the state before each tile, or null
+    float* saved;             // [B, ceil(T / kBwdTile), D]: the state before each of those tiles, or null
     const void* dy;           // [B,T,D] (backward)
     const float* dstate_out;  // [B,D] or null
     void *dv, *df, *dg;       // [B,T,D] (backward; dg null where g is)
@@ -31,8 +33,16 @@ struct ScanParams {
     int y_bf16;     // y and dy
     int grad_bf16;  // dv, df, dg
     int weight;     // 0: 1, 1: 1 - mu, 2: sqrt(1 - mu^2)
+    // Hand-offs between the workgroups of a chain (scan_workspace_bytes), or
+    // null where T is one tile: a ticket counter, then the pairs (layer_chain.h).
+    void* ws;
+    int group;      // tiles per group
 };
 
+// Bytes of ScanParams::ws and the tiles per group, for B sequences of T tokens and D channels.
+size_t scan_workspace_bytes(int B, int T, int D);
+int scan_group(int B, int T, int D);
+void clear_scan_workspace(const ScanParams& p, hipStream_t st);
 // Return 0 or -5 (launch error).
 int launch_scan_fwd(const ScanParams& p, hipStream_t st);
 int launch_scan_bwd(const ScanParams& p, hipStream_t st);

@@ -7,11 +7,13 @@
 // A the product of its mu and H its result from a zero state; two runs in a row
 // compose to (A2 A1, A2 H1 + H2), which is what lets the time axis be split.
 //
-// A workgroup takes 64 V channels (a lane holds V neighbours, so a wave reads
-// one contiguous piece of each token row) and kScanTile tokens at a time; each of its waves
-// takes a run of kRun tokens of the tile, kept in registers as (mu, w gamma v).  The
-// waves' (A, H) meet in LDS, every wave folds those before its own onto the
-// tile's starting state and walks its run once more to form y.
+// A workgroup takes one tile of kFwdTile tokens of 64 V channels (layer_chain.h): a lane
+// holds V neighbouring channels, so a wave reads one contiguous piece of each
+// token row, and each of its waves takes a run of kRun tokens, kept in registers as (mu, w gamma v).
+// The waves' maps meet in LDS, the tile's starting state comes from its
+// chain, every wave folds the runs before its own onto it and walks its run once more to form y.
+// Every input is read once and every output written once.
+#include "layer_chain.h"
 #include "layer_device.h"
 #include "layer_launch.h"
 
@@ -19,16 +21,14 @@ namespace layer {
 namespace {
 
 constexpr int kRun = 16;                   // tokens per wave of a tile
-constexpr int kWaves = kScanTile / kRun;   // waves per workgroup
+constexpr int kWaves = kFwdTile / kRun;   // waves per workgroup
 
 // (mu, w(mu) gamma v) of one element.
 template <int WT, bool GAMMA>
 __device__ __forceinline__ void coefficients(float f, float v, float g, float& a, float& b) {
     float r;
     sigmoid2(f, a, r);
-    b = v;
-    if (WT == 1) b *= r;
-    if (WT == 2) b *= __builtin_amdgcn_sqrtf(r * (1.0f + a));
+    b = v * weight_of<WT>(a, r);
     if (GAMMA) {
         float s, q;
         sigmoid2(g, s, q);
@@ -37,82 +37,119 @@ __device__ __forceinline__ void coefficients(float f, float v, float g, float& a
 }
 
 template <typename TIn, int V, int WT, bool GAMMA>
-__global__ __launch_bounds__(kWaves * 64) void layer_scan_fwd_kernel(ScanParams p) {
+__global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_fwd_kernel(ScanParams p) {
     constexpr int CB = 64 * V;  // channels per workgroup
-    __shared__ float sA[kWaves][CB], sH[kWaves][CB];
+    __shared__ Shared<kWaves, CB> s;
+    __shared__ uint32_t ticket;
     const int nblk = (p.D + CB - 1) / CB;
-    const int b = static_cast<int>(blockIdx.x / nblk);
-    const int c = static_cast<int>(blockIdx.x % nblk) * CB + (threadIdx.x & 63) * V;
-    const int l = (threadIdx.x & 63) * V;
-    const int wave = threadIdx.x >> 6;
-    const bool live = c < p.D;  // V divides D: a lane's channels are all inside or all outside
-    const int cc = live ? c : 0;
-    const TIn* vp = static_cast<const TIn*>(p.v) + static_cast<int64_t>(b) * p.T * p.D + cc;
-    const TIn* fp = static_cast<const TIn*>(p.f) + static_cast<int64_t>(b) * p.T * p.D + cc;
-    const TIn* gp = GAMMA ? static_cast<const TIn*>(p.g) + static_cast<int64_t>(b) * p.T * p.D + cc : nullptr;
-    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
-    const int tiles = (p.T + kScanTile - 1) / kScanTile;
-
-    float carry[V];
-#pragma unroll
-    for (int j = 0; j < V; ++j) carry[j] = p.state_in ? p.state_in[static_cast<int64_t>(b) * p.D + cc + j] : 0.0f;
-
-    for (int tile = 0; tile < tiles; ++tile) {
-        const int t0 = tile * kScanTile + wave * kRun;
-        Vec<TIn, V> rf[kRun], rv[kRun], rg[GAMMA ? kRun : 1];
-#pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            const int64_t row = static_cast<int64_t>(min(t0 + i, p.T - 1)) * p.D;
-            rf[i] = load_vec<TIn, V>(fp, row);
-            rv[i] = load_vec<TIn, V>(vp, row);
-            if (GAMMA) rg[i] = load_vec<TIn, V>(gp, row);
-        }
-        float a[kRun][V], x[kRun][V], A[V], H[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) A[j] = 1.0f, H[j] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kRun; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                coefficients<WT, GAMMA>(widen(rf[i].e[j]), widen(rv[i].e[j]), GAMMA ? widen(rg[i].e[j]) : 0.0f,
-                                        a[i][j], x[i][j]);
-                if (t0 + i >= len) a[i][j] = 1.0f, x[i][j] = 0.0f;
-                A[j] *= a[i][j];
-                H[j] = fmaf(a[i][j], H[j], x[i][j]);
-            }
-        __syncthreads();  // the tile before has been read
-#pragma unroll
-        for (int j = 0; j < V; ++j) sA[wave][l + j] = A[j], sH[wave][l + j] = H[j];
+    const int chains = p.B * nblk;
+    const int tiles = (p.T + kFwdTile - 1) / kFwdTile;
+    uint32_t id = blockIdx.x;
+    if (p.ws) {
+        if (threadIdx.x == 0) ticket = atomicAdd(static_cast<uint32_t*>(p.ws), 1u);
         __syncthreads();
-        if (p.saved && wave == 0 && live) {
+        id = __builtin_amdgcn_readfirstlane(ticket);
+    }
+    const int tile = static_cast<int>(id / chains), chain = static_cast<int>(id % chains);
+    const int b = chain / nblk;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l = (threadIdx.x & 63) * V;
+    const int c = chain % nblk * CB + l;
+    const bool live = c < p.D;  // V divides D: a lane's channels are all inside or all outside
+    const int len = p.lengths ? min(max(p.lengths[b], 0), p.T) : p.T;
+    const int active = max(1, (len + kFwdTile - 1) / kFwdTile);  // tiles with tokens, the first in any case
+    const int t0 = tile * kFwdTile;
+    const int64_t first = (static_cast<int64_t>(b) * p.T + t0) * p.D;
+    const int rows = min(kFwdTile, p.T - t0);
+    const int r0 = wave * kRun;  // this wave's rows of the tile
+    const uint32_t off = (live ? static_cast<uint32_t>(c) : kOut) + static_cast<uint32_t>(r0) * p.D;
+    const auto yr = rows_rsrc(p.y, p.y_bf16, first, rows, p.D);
+    if (tile >= active) {
+        const float zero[V] = {};
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                p.saved[(static_cast<int64_t>(b) * tiles + tile) * p.D + c + j] = carry[j];
+        for (int i = 0; i < kRun; ++i) store_rows<V>(yr, off + i * p.D, zero, p.y_bf16);
+        return;
+    }
+
+    const auto fr = rows_rsrc(static_cast<const TIn*>(p.f) + first, rows, p.D);
+    const auto vr = rows_rsrc(static_cast<const TIn*>(p.v) + first, rows, p.D);
+    const auto gr = rows_rsrc(static_cast<const TIn*>(GAMMA ? p.g : p.f) + first, rows, p.D);
+    Vec<TIn, V> rf[kRun], rv[kRun], rg[GAMMA ? kRun : 1];
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        rf[i] = load_rows<TIn, V>(fr, off + i * p.D);
+        rv[i] = load_rows<TIn, V>(vr, off + i * p.D);
+        if (GAMMA) rg[i] = load_rows<TIn, V>(gr, off + i * p.D);
+    }
+    float before[V] = {};  // the chain's first state
+    const int64_t sc = static_cast<int64_t>(b) * p.D + c;
+    if (p.state_in && live && wave == 0 && tile < (p.ws ? p.group : 1)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) before[j] = p.state_in[sc + j];
+    }
+
+    float a[kRun][V], x[kRun][V], A[V], H[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) A[j] = 1.0f, H[j] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i)
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            coefficients<WT, GAMMA>(widen(rf[i].e[j]), widen(rv[i].e[j]), GAMMA ? widen(rg[i].e[j]) : 0.0f, a[i][j],
+                                    x[i][j]);
+            if (t0 + r0 + i >= len) a[i][j] = 1.0f, x[i][j] = 0.0f;
+            A[j] *= a[i][j];
+            H[j] = fmaf(a[i][j], H[j], x[i][j]);
         }
-        float h[V];
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+    for (int j = 0; j < V; ++j) s.A[wave][l + j] = A[j], s.H[wave][l + j] = H[j];
+    __syncthreads();
+    const bool last = tile == active - 1;
+    if (wave == 0) {
+        // the tile's map
+#pragma unroll 2
+        for (int w = 1; w < kWaves; ++w)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                if (w == wave) h[j] = carry[j];
-                carry[j] = fmaf(sA[w][l + j], carry[j], sH[w][l + j]);
+                H[j] = fmaf(s.A[w][l + j], H[j], s.H[w][l + j]);
+                A[j] *= s.A[w][l + j];
             }
+    }
+    if (p.ws) {
+        chain_carry<V>(s, chain_of(p.ws, chains, tiles, p.group, CB), chain, tile, last, before, A, H);
+    } else {
+        if (wave == 0) {
+#pragma unroll
+            for (int j = 0; j < V; ++j) s.carry[l + j] = before[j];
         }
+        __syncthreads();
+    }
+    float h[V];
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            float o[V];
+    for (int j = 0; j < V; ++j) h[j] = s.carry[l + j];
+    if (wave == 0 && live) {
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                h[j] = fmaf(a[i][j], h[j], x[i][j]);
-                o[j] = t0 + i < len ? h[j] : 0.0f;
-            }
-            if (live && t0 + i < p.T)
-                store_vec<V>(p.y, (static_cast<int64_t>(b) * p.T + t0 + i) * p.D + c, o, p.y_bf16);
+        for (int j = 0; j < V; ++j) {
+            if (p.state_out && last) p.state_out[sc + j] = len > 0 ? fmaf(A[j], h[j], H[j]) : h[j];
         }
     }
-    if (p.state_out && wave == 0 && live) {
+    for (int w = 0; w < wave; ++w)
 #pragma unroll
-        for (int j = 0; j < V; ++j) p.state_out[static_cast<int64_t>(b) * p.D + c + j] = carry[j];
+        for (int j = 0; j < V; ++j) h[j] = fmaf(s.A[w][l + j], h[j], s.H[w][l + j]);
+    if (p.saved && live && r0 % kBwdTile == 0 && r0 < rows) {
+        const int64_t saves = (p.T + kBwdTile - 1) / kBwdTile;
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.saved[(b * saves + (t0 + r0) / kBwdTile) * p.D + c + j] = h[j];
+    }
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) {
+        float o[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            h[j] = fmaf(a[i][j], h[j], x[i][j]);
+            o[j] = t0 + r0 + i < len ? h[j] : 0.0f;
+        }
+        store_rows<V>(yr, off + i * p.D, o, p.y_bf16);
     }
 }
 
@@ -147,7 +184,9 @@ void launch(bool step, const ScanParams& p, hipStream_t st) {
         return;
     }
     const unsigned nblk = static_cast<unsigned>((p.D + 64 * V - 1) / (64 * V));
-    hipLaunchKernelGGL((layer_scan_fwd_kernel<TIn, V, WT, GAMMA>), dim3(nblk * p.B), dim3(kWaves * 64), 0, st, p);
+    const unsigned tiles = static_cast<unsigned>(tiles_of(p.T, kFwdTile));
+    hipLaunchKernelGGL((layer_scan_fwd_kernel<TIn, V, WT, GAMMA>), dim3(nblk * p.B * tiles), dim3(kWaves * 64), 0, st,
+                       p);
 }
 
 template <typename TIn, int V>
@@ -158,6 +197,12 @@ void pick(bool step, const ScanParams& p, hipStream_t st) {
         case 1: g ? launch<TIn, V, 1, true>(step, p, st) : launch<TIn, V, 1, false>(step, p, st); break;
         default: g ? launch<TIn, V, 2, true>(step, p, st) : launch<TIn, V, 2, false>(step, p, st); break;
     }
+}
+
+// Marks every hand-off of the workspace empty and sets the ticket to 0.
+__global__ __launch_bounds__(256) void layer_scan_clear_kernel(uint64_t* ws, int64_t words) {
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < words; i += gridDim.x * 256)
+        ws[i] = i < kTicketBytes / 8 ? 0 : ~UINT64_C(0);
 }
 
 bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -175,7 +220,30 @@ int dispatch(bool step, const ScanParams& p, hipStream_t st) {
 
 }  // namespace
 
-int launch_scan_fwd(const ScanParams& p, hipStream_t st) { return dispatch(false, p, st); }
+int scan_group(int B, int T, int D) {
+    (void)B, (void)T, (void)D;
+    return 16;
+}
+
+size_t scan_workspace_bytes(int B, int T, int D) {
+    const size_t tiles = tiles_of(T, kFwdTile < kBwdTile ? kFwdTile : kBwdTile);
+    if (tiles == 1) return 0;
+    const size_t groups = tiles_of(tiles, scan_group(B, T, D)), width = tiles_of(D, 128) * 128;
+    return kTicketBytes + (tiles + groups) * width * B * sizeof(uint64_t);
+}
+
+void clear_scan_workspace(const ScanParams& p, hipStream_t st) {
+    if (!p.ws) return;
+    const int64_t words = static_cast<int64_t>(scan_workspace_bytes(p.B, p.T, p.D) / 8);
+    const int64_t want = (words + 1023) / 1024;
+    hipLaunchKernelGGL(layer_scan_clear_kernel, dim3(static_cast<unsigned>(want < 1024 ? want : 1024)), dim3(256), 0,
+                       st, static_cast<uint64_t*>(p.ws), words);
+}
+
+int launch_scan_fwd(const ScanParams& p, hipStream_t st) {
+    clear_scan_workspace(p, st);
+    return dispatch(false, p, st);
+}
 int launch_scan_step(const ScanParams& p, hipStream_t st) { return dispatch(true, p, st); }
 
 }  // namespace layer
