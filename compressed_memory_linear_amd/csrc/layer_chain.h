@@ -21,6 +21,8 @@
 // not.  The word is its own flag: no ordering between words is needed.
 #pragma once
 
+#include <type_traits>
+
 #include "layer_device.h"
 #include "layer_launch.h"
 
@@ -62,45 +64,53 @@ __device__ __forceinline__ void get_pair(const uint64_t* p, uint64_t w, float& a
 }
 
 // Rows of a tile as a buffer of their own: an access past the tile's last row, or
-// by a lane without channels (kOut), reads zero and writes nothing.  Offsets
-// count elements; a tile has at most 128 2^20 of them, so kOut (and kOut plus an
-// offset) lies outside and its bytes still fit 32 bits.
-constexpr uint32_t kOut = 0x20000000u;
-template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const T* first, int rows, int D) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(first), 0, rows * D * static_cast<int>(sizeof(T)),
-                                             0x00020000);
-}
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(void* p, bool bf16, int64_t first, int rows, int D) {
-    const int e = bf16 ? 2 : 4;
-    return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(p) + first * e, 0, rows * D * e, 0x00020000);
+// by a lane without channels (kOut), reads zero and writes nothing.  Offsets are in
+// bytes, whole in the address register (the part of the bounds check that needs no
+// care); a tile has at most 2^29, so kOut plus a row's offset lies outside and does not wrap.
+constexpr uint32_t kOut = 0x80000000u;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t first, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, bytes, 0x00020000);
 }
 template <typename T, int V>
 __device__ __forceinline__ Vec<T, V> load_rows(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     constexpr int N = sizeof(T) * V;
     if constexpr (N == 2)
-        return __builtin_bit_cast(Vec<T, V>, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off * 2, 0, 0)));
+        return __builtin_bit_cast(Vec<T, V>, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0)));
     else if constexpr (N == 4)
-        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off * sizeof(T), 0, 0));
+        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
     else
-        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b64(r, off * sizeof(T), 0, 0));
+        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
 }
-template <int V>
-__device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&x)[V], bool bf16) {
+template <int V, bool BF16>
+__device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&x)[V]) {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     static_assert(V == 1 || V == 2, "one or two channels per lane");
-    if (bf16) {
-        if constexpr (V == 1)
-            __builtin_amdgcn_raw_buffer_store_b16(osr::f32_to_bf16_bits(x[0]), r, off * 2, 0, 0);
-        else
-            __builtin_amdgcn_raw_buffer_store_b32(
-                osr::f32_to_bf16_bits(x[0]) | static_cast<uint32_t>(osr::f32_to_bf16_bits(x[1])) << 16, r, off * 2, 0, 0);
-    } else {
-        if constexpr (V == 1)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), r, off * 4, 0, 0);
-        else
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x[0]), __float_as_uint(x[1])}, r, off * 4, 0, 0);
-    }
+    if constexpr (BF16 && V == 1)
+        __builtin_amdgcn_raw_buffer_store_b16(osr::f32_to_bf16_bits(x[0]), r, off, 0, 0);
+    else if constexpr (BF16)
+        __builtin_amdgcn_raw_buffer_store_b32(
+            osr::f32_to_bf16_bits(x[0]) | static_cast<uint32_t>(osr::f32_to_bf16_bits(x[1])) << 16, r, off, 0, 0);
+    else if constexpr (V == 1)
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), r, off, 0, 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x[0]), __float_as_uint(x[1])}, r, off, 0, 0);
+}
+
+// The value, in a register whose origin the compiler does not see: offsets taken from
+// it are formed where they are used and not held from the top of the kernel (16 to 32 registers).
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// f(constant) for a flag that is the same in every thread: one branch around a whole
+// loop instead of one in each of its steps.
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F&& f) {
+    if (flag)
+        f(std::true_type());
+    else
+        f(std::false_type());
 }
 
 // What the waves of a workgroup share: their runs' maps, the composed maps of the tiles

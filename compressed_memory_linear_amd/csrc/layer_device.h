@@ -35,26 +35,32 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&x)[V
     }
 }
 
-// e^x through the hardware's 2^x.  The product x log2(e) is kept in two parts:
-// rounded to one float it would cost a relative |x| 2^-24 of the result.
-__device__ __forceinline__ float exp_acc(float x) {
-    constexpr float kLog2e = 1.44269504088896341f, kLog2eLo = 1.92596299e-8f, kLn2 = 0.693147181f;
+// e^x through the hardware's 2^x.  Rounded to one float, the product x log2(e) costs a
+// relative |x| 2^-24 of the result; ACC keeps its error as a second part (4 operations
+// more).  For bf16 logits, known to 2^-9 of their value, the first form serves.
+template <bool ACC>
+__device__ __forceinline__ float exp_of(float x) {
+    constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147181f;
     const float hi = x * kLog2e;
-    // past the range of 2^x the low part is not wanted (it is NaN at infinite x)
-    const float lo = fmaf(x, kLog2eLo, fmaf(x, kLog2e, -hi));
     const float e = __builtin_amdgcn_exp2f(hi);
+    if constexpr (!ACC) return e;
+    const float lo = fmaf(x, kLog2e, -hi);
+    // past the range of 2^x the low part is not wanted (it is NaN at infinite x)
     return fabsf(hi) < 128.0f ? fmaf(e, lo * kLn2, e) : e;
 }
 
-// s = sigmoid(x) and r = 1 - s, each to a few units of 2^-24 of its own value:
-// with e = e^-x, s = 1 / (1 + e) and r = e s (1 once e is so large that s is
+// s = sigmoid(x) and r = 1 - s, each to a few units of 2^-24 of its own value (ACC as
+// above): with e = e^-x, s = 1 / (1 + e) and r = e s (1 once e is so large that s is
 // below half a unit of 1; the product would be inf 0 there).  x = -inf gives
 // s = 0, r = 1 and x = +inf gives s = 1, r = 0, exactly; NaN stays NaN.
+template <bool ACC>
 __device__ __forceinline__ void sigmoid2(float x, float& s, float& r) {
-    const float e = exp_acc(-x);
+    const float e = exp_of<ACC>(-x);
     s = __builtin_amdgcn_rcpf(1.0f + e);
     r = e > 33554432.0f ? 1.0f : e * s;
 }
+template <typename T>
+constexpr bool kAccurate = sizeof(T) == 4;  // logits of type T
 
 // The scan's input weight w(mu), from mu and 1 - mu.
 template <int WT>

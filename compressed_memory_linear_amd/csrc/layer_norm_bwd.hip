@@ -65,14 +65,14 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
                     const float g = widen(rg.e[e]);
                     const float cdf = 0.5f * erfcf(-g * 0.70710678118654752f);
                     phi[k][e] = g * cdf;
-                    dphi[k][e] = fmaf(g * 0.39894228040143268f, exp_acc(-0.5f * g * g), cdf);
+                    dphi[k][e] = fmaf(g * 0.39894228040143268f, exp_of<true>(-0.5f * g * g), cdf);
                 }
             } else if (p.gate_kind == 2) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
                     const float g = widen(rg.e[e]);
                     float s, r;
-                    sigmoid2(g, s, r);
+                    sigmoid2<true>(g, s, r);
                     phi[k][e] = g * s;
                     dphi[k][e] = s * fmaf(g, r, 1.0f);
                 }

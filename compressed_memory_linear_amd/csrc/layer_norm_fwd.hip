@@ -50,7 +50,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
                 for (int e = 0; e < kE; ++e) {
                     const float g = widen(rg.e[e]);
                     float s, r;
-                    sigmoid2(g, s, r);
+                    sigmoid2<true>(g, s, r);
                     u[k][e] *= g * s;
                 }
             }

@@ -24,14 +24,14 @@ constexpr int kRun = 16;                   // tokens per wave of a tile
 constexpr int kWaves = kFwdTile / kRun;   // waves per workgroup
 
 // (mu, w(mu) gamma v) of one element.
-template <int WT, bool GAMMA>
+template <int WT, bool GAMMA, bool ACC>
 __device__ __forceinline__ void coefficients(float f, float v, float g, float& a, float& b) {
     float r;
-    sigmoid2(f, a, r);
+    sigmoid2<ACC>(f, a, r);
     b = v * weight_of<WT>(a, r);
     if (GAMMA) {
         float s, q;
-        sigmoid2(g, s, q);
+        sigmoid2<ACC>(g, s, q);
         b *= s;
     }
 }
@@ -62,24 +62,29 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_fwd_kernel(ScanPara
     const int64_t first = (static_cast<int64_t>(b) * p.T + t0) * p.D;
     const int rows = min(kFwdTile, p.T - t0);
     const int r0 = wave * kRun;  // this wave's rows of the tile
-    const uint32_t off = (live ? static_cast<uint32_t>(c) : kOut) + static_cast<uint32_t>(r0) * p.D;
-    const auto yr = rows_rsrc(p.y, p.y_bf16, first, rows, p.D);
+    // byte offsets of this lane's channels in the wave's first row, and from row to row
+    const int ey = p.y_bf16 ? 2 : 4;
+    const uint32_t oin = live ? (static_cast<uint32_t>(r0) * p.D + c) * sizeof(TIn) : kOut, din = p.D * sizeof(TIn);
+    const uint32_t oy = live ? (static_cast<uint32_t>(r0) * p.D + c) * ey : kOut, dyo = p.D * ey;
+    const auto yr = rows_rsrc(p.y, first * ey, rows * p.D * ey);
     if (tile >= active) {
         const float zero[V] = {};
+        with_flag(p.y_bf16, [&](auto bf16) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) store_rows<V>(yr, off + i * p.D, zero, p.y_bf16);
+            for (int i = 0; i < kRun; ++i) store_rows<V, bf16()>(yr, oy + i * dyo, zero);
+        });
         return;
     }
 
-    const auto fr = rows_rsrc(static_cast<const TIn*>(p.f) + first, rows, p.D);
-    const auto vr = rows_rsrc(static_cast<const TIn*>(p.v) + first, rows, p.D);
-    const auto gr = rows_rsrc(static_cast<const TIn*>(GAMMA ? p.g : p.f) + first, rows, p.D);
+    const auto fr = rows_rsrc(p.f, first * sizeof(TIn), rows * p.D * sizeof(TIn));
+    const auto vr = rows_rsrc(p.v, first * sizeof(TIn), rows * p.D * sizeof(TIn));
+    const auto gr = rows_rsrc(GAMMA ? p.g : p.f, first * sizeof(TIn), rows * p.D * sizeof(TIn));
     Vec<TIn, V> rf[kRun], rv[kRun], rg[GAMMA ? kRun : 1];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-        rf[i] = load_rows<TIn, V>(fr, off + i * p.D);
-        rv[i] = load_rows<TIn, V>(vr, off + i * p.D);
-        if (GAMMA) rg[i] = load_rows<TIn, V>(gr, off + i * p.D);
+        rf[i] = load_rows<TIn, V>(fr, oin + i * din);
+        rv[i] = load_rows<TIn, V>(vr, oin + i * din);
+        if (GAMMA) rg[i] = load_rows<TIn, V>(gr, oin + i * din);
     }
     float before[V] = {};  // the chain's first state
     const int64_t sc = static_cast<int64_t>(b) * p.D + c;
@@ -95,12 +100,26 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_fwd_kernel(ScanPara
     for (int i = 0; i < kRun; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            coefficients<WT, GAMMA>(widen(rf[i].e[j]), widen(rv[i].e[j]), GAMMA ? widen(rg[i].e[j]) : 0.0f, a[i][j],
-                                    x[i][j]);
-            if (t0 + r0 + i >= len) a[i][j] = 1.0f, x[i][j] = 0.0f;
+            coefficients<WT, GAMMA, kAccurate<TIn>>(widen(rf[i].e[j]), widen(rv[i].e[j]),
+                                                    GAMMA ? widen(rg[i].e[j]) : 0.0f, a[i][j], x[i][j]);
             A[j] *= a[i][j];
             H[j] = fmaf(a[i][j], H[j], x[i][j]);
         }
+    // Padding keeps the state.  Set right afterwards, in the one tile that has both, so that the
+    // others pay nothing.
+    const bool padded = t0 + kFwdTile > len;
+    if (padded) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) A[j] = 1.0f, H[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (t0 + r0 + i >= len) a[i][j] = 1.0f, x[i][j] = 0.0f;
+                A[j] *= a[i][j];
+                H[j] = fmaf(a[i][j], H[j], x[i][j]);
+            }
+    }
 #pragma unroll
     for (int j = 0; j < V; ++j) s.A[wave][l + j] = A[j], s.H[wave][l + j] = H[j];
     __syncthreads();
@@ -142,15 +161,21 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_fwd_kernel(ScanPara
         for (int j = 0; j < V; ++j) p.saved[(b * saves + (t0 + r0) / kBwdTile) * p.D + c + j] = h[j];
     }
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-        float o[V];
+    for (int i = 0; i < kRun; ++i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            h[j] = fmaf(a[i][j], h[j], x[i][j]);
-            o[j] = t0 + r0 + i < len ? h[j] : 0.0f;
-        }
-        store_rows<V>(yr, off + i * p.D, o, p.y_bf16);
+        for (int j = 0; j < V; ++j) x[i][j] = h[j] = fmaf(a[i][j], h[j], x[i][j]);
+    if (padded) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (t0 + r0 + i >= len) x[i][j] = 0.0f;
     }
+    with_flag(p.y_bf16, [&](auto bf16) {
+        const uint32_t to = here(oy);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) store_rows<V, bf16()>(yr, to + i * dyo, x[i]);
+    });
 }
 
 // One token: state_out may be state_in (each channel is read, then written, by one thread).
@@ -168,7 +193,7 @@ __global__ __launch_bounds__(64) void layer_scan_step_kernel(ScanParams p) {
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         float a, x;
-        coefficients<WT, GAMMA>(widen(f.e[j]), widen(v.e[j]), widen(g.e[j]), a, x);
+        coefficients<WT, GAMMA, kAccurate<TIn>>(widen(f.e[j]), widen(v.e[j]), widen(g.e[j]), a, x);
         h[j] = fmaf(a, s.e[j], x);
     }
     store_vec<V>(p.state_out, i, h, false);

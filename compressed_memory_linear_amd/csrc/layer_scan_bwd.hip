@@ -47,33 +47,40 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_bwd_kernel(ScanPara
     const int64_t first = (static_cast<int64_t>(b) * p.T + t0) * p.D;
     const int rows = min(kBwdTile, p.T - t0);
     const int r0 = wave * kRun;
-    const uint32_t off = (live ? static_cast<uint32_t>(c) : kOut) + static_cast<uint32_t>(r0) * p.D;
-    const auto dvr = rows_rsrc(p.dv, p.grad_bf16, first, rows, p.D);
-    const auto dfr = rows_rsrc(p.df, p.grad_bf16, first, rows, p.D);
-    const auto dgr = rows_rsrc(GAMMA ? p.dg : p.df, p.grad_bf16, first, rows, p.D);
+    const int eg = p.grad_bf16 ? 2 : 4;
+    const uint32_t at = static_cast<uint32_t>(r0) * p.D + c;
+    const uint32_t oin = live ? at * sizeof(TIn) : kOut, din = p.D * sizeof(TIn);
+    const uint32_t ody = live ? at * sizeof(TDy) : kOut, ddy = p.D * sizeof(TDy);
+    const uint32_t og = live ? at * eg : kOut, dog = p.D * eg;
+    const auto dvr = rows_rsrc(p.dv, first * eg, rows * p.D * eg);
+    const auto dfr = rows_rsrc(p.df, first * eg, rows * p.D * eg);
+    const auto dgr = rows_rsrc(GAMMA ? p.dg : p.df, first * eg, rows * p.D * eg);
     if (tile >= active) {
         const float zero[V] = {};
+        with_flag(p.grad_bf16, [&](auto bf16) {
 #pragma unroll
-        for (int i = 0; i < kRun; ++i) {
-            store_rows<V>(dvr, off + i * p.D, zero, p.grad_bf16);
-            store_rows<V>(dfr, off + i * p.D, zero, p.grad_bf16);
-            if (GAMMA) store_rows<V>(dgr, off + i * p.D, zero, p.grad_bf16);
-        }
+            for (int i = 0; i < kRun; ++i) {
+                store_rows<V, bf16()>(dvr, og + i * dog, zero);
+                store_rows<V, bf16()>(dfr, og + i * dog, zero);
+                if (GAMMA) store_rows<V, bf16()>(dgr, og + i * dog, zero);
+            }
+        });
         return;
     }
 
-    const auto fr = rows_rsrc(static_cast<const TIn*>(p.f) + first, rows, p.D);
-    const auto vr = rows_rsrc(static_cast<const TIn*>(p.v) + first, rows, p.D);
-    const auto gr = rows_rsrc(static_cast<const TIn*>(GAMMA ? p.g : p.f) + first, rows, p.D);
-    const auto yr = rows_rsrc(static_cast<const TDy*>(p.dy) + first, rows, p.D);
+    const int nin = rows * p.D * static_cast<int>(sizeof(TIn));
+    const auto fr = rows_rsrc(p.f, first * sizeof(TIn), nin);
+    const auto vr = rows_rsrc(p.v, first * sizeof(TIn), nin);
+    const auto gr = rows_rsrc(GAMMA ? p.g : p.f, first * sizeof(TIn), nin);
+    const auto yr = rows_rsrc(p.dy, first * sizeof(TDy), rows * p.D * static_cast<int>(sizeof(TDy)));
     Vec<TIn, V> rf[kRun], rv[kRun], rg[GAMMA ? kRun : 1];
     Vec<TDy, V> ry[kRun];
 #pragma unroll
     for (int i = 0; i < kRun; ++i) {
-        rf[i] = load_rows<TIn, V>(fr, off + i * p.D);
-        rv[i] = load_rows<TIn, V>(vr, off + i * p.D);
-        if (GAMMA) rg[i] = load_rows<TIn, V>(gr, off + i * p.D);
-        ry[i] = load_rows<TDy, V>(yr, off + i * p.D);
+        rf[i] = load_rows<TIn, V>(fr, oin + i * din);
+        rv[i] = load_rows<TIn, V>(vr, oin + i * din);
+        if (GAMMA) rg[i] = load_rows<TIn, V>(gr, oin + i * din);
+        ry[i] = load_rows<TDy, V>(yr, ody + i * ddy);
     }
     float h[V] = {}, behind[V] = {};  // the state before the tile, the chain's first gradient
     const int rank = active - 1 - tile;
@@ -90,29 +97,40 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_bwd_kernel(ScanPara
     float a[kRun][V], om[kRun][V], gam[GAMMA ? kRun : 1][V], A[V], H[V], R[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) A[j] = 1.0f, H[j] = 0.0f, R[j] = 0.0f;
+    auto run_map = [&](int i, int j) {
+        const float x = widen(rv[i].e[j]) * weight_of<WT>(a[i][j], om[i][j]);
+        A[j] *= a[i][j];
+        H[j] = fmaf(a[i][j], H[j], GAMMA ? x * gam[GAMMA ? i : 0][j] : x);
+    };
 #pragma unroll
     for (int i = 0; i < kRun; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const bool in = t0 + r0 + i < len;
-            sigmoid2(widen(rf[i].e[j]), a[i][j], om[i][j]);
-            float x = widen(rv[i].e[j]) * weight_of<WT>(a[i][j], om[i][j]);
+            sigmoid2<kAccurate<TIn>>(widen(rf[i].e[j]), a[i][j], om[i][j]);
             if (GAMMA) {
                 float q;
-                sigmoid2(widen(rg[i].e[j]), gam[i][j], q);
-                x *= gam[i][j];
+                sigmoid2<kAccurate<TIn>>(widen(rg[i].e[j]), gam[i][j], q);
             }
-            if (!in) a[i][j] = 1.0f, x = 0.0f;
-            A[j] *= a[i][j];
-            H[j] = fmaf(a[i][j], H[j], x);
+            run_map(i, j);
         }
+    // Padding passes the gradient on and keeps the state.  Set right afterwards, in the one tile
+    // that has both, so that the others pay nothing.
+    const bool padded = t0 + kBwdTile > len;
+    if (padded) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) A[j] = 1.0f, H[j] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (t0 + r0 + i >= len) a[i][j] = 1.0f, rv[i].e[j] = TIn(0), ry[i].e[j] = TDy(0);
+                run_map(i, j);
+            }
+    }
 #pragma unroll
     for (int i = kRun - 1; i >= 0; --i)
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const float dy = t0 + r0 + i < len ? widen(ry[i].e[j]) : 0.0f;
-            R[j] = a[i][j] * (dy + R[j]);
-        }
+        for (int j = 0; j < V; ++j) R[j] = a[i][j] * (R[j] + widen(ry[i].e[j]));
 #pragma unroll
     for (int j = 0; j < V; ++j) s.A[wave][l + j] = A[j], s.H[wave][l + j] = R[j], sH[wave][l + j] = H[j];
     __syncthreads();
@@ -159,38 +177,49 @@ __global__ __launch_bounds__(kWaves * 64, 4) void layer_scan_bwd_kernel(ScanPara
     for (int i = 0; i < kRun; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const bool in = t0 + r0 + i < len;
             const float m = a[i][j], o = om[i][j], w = weight_of<WT>(m, o);
-            const float gx = GAMMA ? gam[i][j] * widen(rv[i].e[j]) : widen(rv[i].e[j]);
-            wg[i][j] = GAMMA ? w * gam[i][j] : w;
-            float into = m * o * h[j];
-            if (WT == 1) into = fmaf(-m * o, gx, into);
-            if (WT == 2) into = fmaf(-m * m * w * __builtin_amdgcn_rcpf(1.0f + m), gx, into);
-            om[i][j] = into;
-            if (GAMMA) {
+            const float gx = GAMMA ? gam[GAMMA ? i : 0][j] * widen(rv[i].e[j]) : widen(rv[i].e[j]);
+            wg[i][j] = GAMMA ? w * gam[GAMMA ? i : 0][j] : w;
+            if constexpr (WT == 0) om[i][j] = m * o * h[j];
+            if constexpr (WT == 1) om[i][j] = m * o * (h[j] - gx);
+            if constexpr (WT == 2) om[i][j] = m * fmaf(o, h[j], -m * w * __builtin_amdgcn_rcpf(1.0f + m) * gx);
+            if constexpr (GAMMA) {
                 float q, ng;
-                sigmoid2(widen(rg[i].e[j]), q, ng);
+                sigmoid2<kAccurate<TIn>>(widen(rg[i].e[j]), q, ng);
                 gam[i][j] = w * gx * ng;
             }
-            h[j] = in ? fmaf(m, h[j], w * gx) : h[j];
+            h[j] = fmaf(m, h[j], w * gx);
         }
-    // Third pass, backwards: the gradients.
+    // Third pass, backwards: the gradients, in the factors' places.
 #pragma unroll
-    for (int i = kRun - 1; i >= 0; --i) {
-        float dv[V], df[V], dg[V];
-        const bool in = t0 + r0 + i < len;
+    for (int i = kRun - 1; i >= 0; --i)
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const float lam = (in ? widen(ry[i].e[j]) : 0.0f) + r[j];
-            dv[j] = in ? lam * wg[i][j] : 0.0f;
-            df[j] = in ? lam * om[i][j] : 0.0f;
-            if (GAMMA) dg[j] = in ? lam * gam[i][j] : 0.0f;
+            const float lam = widen(ry[i].e[j]) + r[j];
+            wg[i][j] *= lam;
+            om[i][j] *= lam;
+            if constexpr (GAMMA) gam[i][j] *= lam;
             r[j] = a[i][j] * lam;
         }
-        store_rows<V>(dvr, off + i * p.D, dv, p.grad_bf16);
-        store_rows<V>(dfr, off + i * p.D, df, p.grad_bf16);
-        if (GAMMA) store_rows<V>(dgr, off + i * p.D, dg, p.grad_bf16);
+    if (padded) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (t0 + r0 + i >= len) {
+                    wg[i][j] = om[i][j] = 0.0f;
+                    if constexpr (GAMMA) gam[i][j] = 0.0f;
+                }
     }
+    with_flag(p.grad_bf16, [&](auto bf16) {
+        const uint32_t to = here(og);
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            store_rows<V, bf16()>(dvr, to + i * dog, wg[i]);
+            store_rows<V, bf16()>(dfr, to + i * dog, om[i]);
+            if constexpr (GAMMA) store_rows<V, bf16()>(dgr, to + i * dog, gam[i]);
+        }
+    });
 }
 
 template <typename TIn, typename TDy, int V, int WT, bool GAMMA>

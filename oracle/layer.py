@@ -24,10 +24,13 @@ TINY = 1e-35  # what flushing subnormal numbers may cost
 ONE, COMPLEMENT, NORM = 0, 1, 2
 NONE, GELU, SILU = 0, 1, 2
 
-# sigmoid: e = 2^(x log2 e) off by 6 u (the argument is kept in two parts; 2^x 2 u,
-# its correction 2 u, what is left of the argument 2 u), 1 + e and 1 / x 3 u more; e s one more.
+# sigmoid(x): e = 2^(x log2 e) off by |x| u (the rounded product; the callers that keep it in two
+# parts do better) and 6 u, 1 + e and 1 / x 3 u more; e s one more.
 E_SIG = 10 * U
-E_COEF = 32 * U  # w(mu) gamma v: two gates, a root (half of its argument's error, 2 u of its own), three products
+
+
+def _e_sig(x):
+    return E_SIG + U * x.abs().clamp(max=100.0)
 
 
 # ----------------------------------------------------------------- scan --
@@ -57,6 +60,9 @@ def scan(v, f, g=None, state_in=None, lengths=None, weight=COMPLEMENT, dy=None, 
     ok = _valid(lengths, B, T, dev)
     v, mu, om, gam, ngam, w, pull = _gates(v, f, g, weight)
     z = torch.zeros((), dtype=torch.float64, device=dev)
+    es = torch.where(ok, _e_sig(f.double()), z)                               # of mu and 1 - mu
+    eg = torch.where(ok, _e_sig(g.double()), z) if g is not None else z + 0 * es  # of gamma
+    ec = es + eg + 12 * U  # of w(mu) gamma v: both gates, a root (its own 2 u), its argument, three products
     a = torch.where(ok, mu, z + 1)
     b = torch.where(ok, w * gam * v, z)
     h = torch.zeros((B, D), dtype=torch.float64, device=dev) if state_in is None else state_in.double()
@@ -69,7 +75,7 @@ def scan(v, f, g=None, state_in=None, lengths=None, weight=COMPLEMENT, dy=None, 
         h = a[:, t] * h + b[:, t]
         s = a[:, t] * s + b[:, t].abs()
         # a's error, the rounding of the step and of the composition of runs, b's error
-        e = a[:, t] * e + torch.where(ok[:, t], (E_SIG + E_COEF + 4 * U) * s, z)
+        e = a[:, t] * e + torch.where(ok[:, t], (es[:, t] + ec[:, t] + 4 * U) * s, z)
         H.append(h)
     H, before, S, E = (torch.stack(x, 1) for x in (H, before, S, E))
     # the error of h after token t is that before token t + 1
@@ -84,20 +90,20 @@ def scan(v, f, g=None, state_in=None, lengths=None, weight=COMPLEMENT, dy=None, 
     gx = gam * v
     into = mu * om * before + pull * gx
     sinto = mu * om * S + (pull * gx).abs()
-    einto = mu * om * E + 6 * E_SIG * sinto
+    einto = mu * om * E + (4 * es + eg + 16 * U) * sinto
     names = ("dmu_logit", "dv", "dgamma_logit")
     got, lim = {n: [] for n in names}, {n: [] for n in names}
     for t in range(T - 1, -1, -1):
         lam = lam + dy[:, t]
         sl = sl + dy[:, t].abs()
         el = el + 2 * U * sl
-        for n, c, ec in (("dmu_logit", into[:, t], einto[:, t]), ("dv", (w * gam)[:, t], E_COEF * (w * gam)[:, t]),
-                         ("dgamma_logit", (w * gx * ngam)[:, t], (E_COEF + E_SIG) * (w * gx * ngam)[:, t].abs())):
+        for n, c, ce in (("dmu_logit", into[:, t], einto[:, t]), ("dv", (w * gam)[:, t], (ec * w * gam)[:, t]),
+                         ("dgamma_logit", (w * gx * ngam)[:, t], ((ec + eg) * (w * gx * ngam).abs())[:, t])):
             size = sinto[:, t] if n == "dmu_logit" else c.abs()
             got[n].append(torch.where(ok[:, t], lam * c, z))
-            lim[n].append(torch.where(ok[:, t], el * size + sl * (ec + 2 * U * size), z) + TINY)
+            lim[n].append(torch.where(ok[:, t], el * size + sl * (ce + 2 * U * size), z) + TINY)
         lam, sl = a[:, t] * lam, a[:, t] * sl
-        el = a[:, t] * el + torch.where(ok[:, t], (E_SIG + 4 * U) * sl, z)
+        el = a[:, t] * el + torch.where(ok[:, t], (es[:, t] + 4 * U) * sl, z)
     for n in names:
         out[n] = torch.stack(got[n][::-1], 1)
         bound[n] = torch.stack(lim[n][::-1], 1)
@@ -117,7 +123,7 @@ def _act(kind, g):
         rel = 2.0 ** -20 + 2 * g * g * U + 4 * U
         return g * cdf, cdf + g * pdf, rel, rel * cdf + (g * pdf).abs() * (16 * U + g * g * U) + 2 * U
     s, r = torch.sigmoid(g), torch.sigmoid(-g)
-    return g * s, s * (1 + g * r), (E_SIG + 2 * U) + 0 * g, (3 * E_SIG + 4 * U) * s * (1 + (g * r).abs())
+    return g * s, s * (1 + g * r), _e_sig(g) + 2 * U, (3 * _e_sig(g) + 4 * U) * s * (1 + (g * r).abs())
 
 
 def norm(y=None, x=None, gate=None, gate_kind=GELU, post=True, w_post=None, scale=None, pre=True, w_pre=None, eps=1e-6,
