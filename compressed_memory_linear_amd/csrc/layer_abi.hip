@@ -144,13 +144,13 @@ int lattice_osr_scan_fwd(const lattice_osr_scan_desc* desc, const void* v, const
                         {state_out, nb * 4, 4, true},
                         {y, n * ey, ey, true},
                         {saved, scan_saved_bytes(desc), 4, true},
-                        {need ? workspace : nullptr, need, 8, true}};
+                        {need ? workspace : nullptr, need, 16, true}};
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
     layer::ScanParams p = scan_params(desc);
     p.v = v, p.f = mu_logit, p.g = gamma_logit, p.lengths = lengths;
     p.state_in = state_in, p.state_out = state_out, p.y = y, p.saved = static_cast<float*>(saved);
-    p.ws = need ? workspace : nullptr, p.group = layer::scan_group(desc->B, desc->T, desc->D);
+    p.ws = need ? workspace : nullptr;
     return layer::launch_scan_fwd(p, static_cast<hipStream_t>(hip_stream));
 }
 
@@ -180,14 +180,14 @@ int lattice_osr_scan_bwd(const lattice_osr_scan_desc* desc, const void* v, const
                         {dmu_logit, n * eg, eg, true},
                         {dgamma_logit, n * eg, eg, true},
                         {dstate_in, nb * 4, 4, true},
-                        {need ? workspace : nullptr, need, 8, true}};
+                        {need ? workspace : nullptr, need, 16, true}};
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
     layer::ScanParams p = scan_params(desc);
     p.v = v, p.f = mu_logit, p.g = gamma_logit, p.lengths = lengths;
     p.saved = const_cast<float*>(static_cast<const float*>(saved));
     p.dy = dy, p.dstate_out = dstate_out;
-    p.ws = need ? workspace : nullptr, p.group = layer::scan_group(desc->B, desc->T, desc->D);
+    p.ws = need ? workspace : nullptr;
     p.dv = dv, p.df = dmu_logit, p.dg = dgamma_logit, p.dstate_in = dstate_in;
     return layer::launch_scan_bwd(p, static_cast<hipStream_t>(hip_stream));
 }

@@ -1,24 +1,32 @@
 // layer_chain.h -- the scan's tiles and the hand-off between their workgroups.
 //
-// The time axis is cut into tiles and the channels into
-// blocks of 64 V; a workgroup takes one tile of one block of one sequence (a
+// The time axis is cut into tiles and the channels into blocks of 64, one to a
+// lane; a workgroup takes one tile of one block of one sequence (a
 // chain), reads it once, and needs from the rest of its chain only the state
 // before the tile (forward; in the backward, which runs the tiles from the last to
 // the first, the gradient from behind it).  A tile maps that state by
 // h -> A h + H, and its (A, H) does not depend on the tiles before it, so it is
-// published at once.  Tiles come in groups of `group`: a tile composes the maps of the
-// tiles before it in its group, waits for the state before the group, and the
-// group's last tile hands the state behind it on.  So a chain waits once per
-// group instead of once per tile, and every sum has a fixed order.
+// published at once.  Tiles come in groups of W = kScanWaves and groups in
+// supergroups of W: a group's last tile composes the group's map and publishes that
+// too, a supergroup's last tile hands the state behind it on.  A tile composes the
+// maps of the tiles before it in its group and of the groups before it in its
+// supergroup, and waits for the state before the supergroup.  So a chain waits for
+// another's state once per W^2 tiles (16384 tokens in the forward), everything else is
+// there as soon as the tiles before have been read, and every sum has a fixed order.
 //
-// Which tile a workgroup takes follows a ticket that it draws when it starts
-// (tiles of all chains in turn): whatever a workgroup waits for belongs to a lower
-// ticket, so its owner has started, and the first unfinished ticket waits for
-// nothing that is unfinished; every wait ends, whatever the order of dispatch.
+// Which tile a workgroup takes follows a ticket that it draws when it starts (one
+// tile of every chain, then the next of every chain): whatever a workgroup waits for
+// belongs to a lower ticket, so its owner has started, and the first unfinished ticket
+// waits for nothing that is unfinished.  Every wait ends, whatever the order of dispatch.
 //
 // A hand-off is a pair of floats stored and loaded as one 64-bit word at agent
-// scope.  The fill kernel in front marks all words empty; a word is read until it is
+// scope.  A kernel in front marks all words empty; a word is read until it is
 // not.  The word is its own flag: no ordering between words is needed.
+//
+// Long runs of narrow blocks measured best (B8 T4096 and, with the writing intensity, B1
+// T65536 at D2048 bf16, forward): two channels a lane with 16 tokens a wave 85 and 219 us, one
+// with 16 120 and 241, one with 24 94 and 206, one with 32 83 and 200; fewer tiles in
+// flight per chain wait less for one another, and 32 tokens are what 128 registers hold.
 #pragma once
 
 #include <type_traits>
@@ -31,15 +39,13 @@ namespace layer {
 constexpr uint32_t kEmpty = 0xffffffffu;  // of the pair's first half
 constexpr int kTicketBytes = 64;
 
-// Words of a chain block: [chain][tile][64 V] maps, then [chain][group][64 V] states.
+// The hand-off words of all chains: [chain][tile][64] maps, [chain][group][64]
+// maps, [chain][supergroup][64] states (the first of each chain unused).
 struct Chain {
-    uint64_t *maps, *states;
-    int tiles, groups, group, width;
-    __device__ __forceinline__ uint64_t* map_at(int chain, int tile) const {
-        return maps + (static_cast<int64_t>(chain) * tiles + tile) * width;
-    }
-    __device__ __forceinline__ uint64_t* state_at(int chain, int g) const {
-        return states + (static_cast<int64_t>(chain) * groups + g) * width;
+    uint64_t *maps, *group_maps, *states;
+    int tiles, groups, supers;
+    __device__ __forceinline__ uint64_t* at(uint64_t* base, int chain, int count, int i) const {
+        return base + (static_cast<int64_t>(chain) * count + i) * 64;
     }
 };
 
@@ -66,34 +72,29 @@ __device__ __forceinline__ void get_pair(const uint64_t* p, uint64_t w, float& a
 // Rows of a tile as a buffer of their own: an access past the tile's last row, or
 // by a lane without channels (kOut), reads zero and writes nothing.  Offsets are in
 // bytes, whole in the address register (the part of the bounds check that needs no
-// care); a tile has at most 2^29, so kOut plus a row's offset lies outside and does not wrap.
+// care); a tile has at most 2^30, so kOut plus a row's offset lies outside and does not wrap.
 constexpr uint32_t kOut = 0x80000000u;
+// Streamed once, rows are loaded non-temporally (B8 T4096 D2048 bf16 forward 90 -> 83 us; inputs that
+// the 256 MB cache still holds lose: B7 T1531 D1001 fp32 36 -> 40).  The backward's stores too
+// (training step 322 -> 306 us); not the forward's, whose y the next kernel reads.
+constexpr int kNt = 2;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t first, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, bytes, 0x00020000);
 }
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> load_rows(__amdgpu_buffer_rsrc_t r, uint32_t off) {
-    constexpr int N = sizeof(T) * V;
-    if constexpr (N == 2)
-        return __builtin_bit_cast(Vec<T, V>, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0)));
-    else if constexpr (N == 4)
-        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+template <typename T>
+__device__ __forceinline__ T load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (sizeof(T) == 2)
+        return __builtin_bit_cast(T, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kNt)));
     else
-        return __builtin_bit_cast(Vec<T, V>, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kNt));
 }
-template <int V, bool BF16>
-__device__ __forceinline__ void store_rows(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&x)[V]) {
-    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-    static_assert(V == 1 || V == 2, "one or two channels per lane");
-    if constexpr (BF16 && V == 1)
-        __builtin_amdgcn_raw_buffer_store_b16(osr::f32_to_bf16_bits(x[0]), r, off, 0, 0);
-    else if constexpr (BF16)
-        __builtin_amdgcn_raw_buffer_store_b32(
-            osr::f32_to_bf16_bits(x[0]) | static_cast<uint32_t>(osr::f32_to_bf16_bits(x[1])) << 16, r, off, 0, 0);
-    else if constexpr (V == 1)
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[0]), r, off, 0, 0);
+// NT: written past the caches.
+template <bool BF16, bool NT>
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off, float x) {
+    if constexpr (BF16)
+        __builtin_amdgcn_raw_buffer_store_b16(osr::f32_to_bf16_bits(x), r, off, 0, NT ? kNt : 0);
     else
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x[0]), __float_as_uint(x[1])}, r, off, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, NT ? kNt : 0);
 }
 
 // The value, in a register whose origin the compiler does not see: offsets taken from
@@ -113,103 +114,123 @@ __device__ __forceinline__ void with_flag(bool flag, F&& f) {
         f(std::false_type());
 }
 
-// What the waves of a workgroup share: their runs' maps, the composed maps of the tiles
-// before, the state before the tile.
-template <int W, int CB>
+// What the waves of a workgroup share: their runs' maps, those of the tiles and of
+// the groups before, the state before the tile.
 struct Shared {
-    float A[W][CB], H[W][CB];
-    float PA[W][CB], PH[W][CB];
-    float carry[CB];
+    float A[kScanWaves][64], H[kScanWaves][64];
+    float PA[kScanWaves][64], PH[kScanWaves][64];
+    float GA[kScanWaves][64], GH[kScanWaves][64];
+    float carry[64];
 };
 
-// The state before this workgroup's tile, into s.carry (every wave calls this; barriers inside).
-// Wave 0 holds the tile's own map (A, H) and the state before the chain, `first`.
+// The state before this workgroup's tile, into s.carry.  Every count is the number
+// of waves W: wave w fetches the map of the w-1st tile of the group and of the w-1st group of
+// the supergroup, wave 0 the state before the supergroup, all asked for together (begin)
+// while the waves' own maps meet in LDS.
 // rank: the tile's place in its chain; last: no tile follows.
-template <int V, int W, int CB>
-__device__ __forceinline__ void chain_carry(Shared<W, CB>& s, const Chain& c, int chain, int rank, bool last,
-                                            float (&first)[V], float (&A)[V], const float (&H)[V]) {
-    const int wave = threadIdx.x >> 6, l = (threadIdx.x & 63) * V;
-    const int g = rank / c.group, before = rank - g * c.group;
-    const bool closes = before + 1 == c.group;
-    if (wave == 0 && !last && !closes) {
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            // the map goes out after `first` has come in: the chain's last tile, which waits for
-            // the map, may write its result where `first` was read
-            asm volatile("" : "+v"(A[j]), "+v"(first[j]));
-            put_pair(c.map_at(chain, rank) + l + j, A[j], H[j]);
+struct Carry {
+    static constexpr int W = kScanWaves;
+    Shared& s;
+    const Chain& c;
+    int chain, rank, wave, l;
+    uint64_t wm, wg;  // wave 0: wm the state
+
+    __device__ __forceinline__ int group() const { return rank / W; }
+    __device__ __forceinline__ int super() const { return rank / (W * W); }
+    __device__ __forceinline__ int tiles_before() const { return rank % W; }
+    __device__ __forceinline__ int groups_before() const { return group() % W; }
+    __device__ __forceinline__ uint64_t* map(int t) const { return c.at(c.maps, chain, c.tiles, t) + l; }
+    __device__ __forceinline__ uint64_t* group_map(int g) const { return c.at(c.group_maps, chain, c.groups, g) + l; }
+    __device__ __forceinline__ uint64_t* state(int k) const { return c.at(c.states, chain, c.supers, k) + l; }
+    __device__ __forceinline__ uint64_t* my_map() const { return map(group() * W + wave - 1); }
+    __device__ __forceinline__ uint64_t* my_group_map() const { return group_map(super() * W + wave - 1); }
+
+    // Ask once; every wave, before the barrier that completes s.A and s.H.
+    __device__ __forceinline__ void begin() {
+        wm = wg = ~UINT64_C(0);
+        if (wave == 0 ? super() > 0 : wave <= tiles_before()) wm = peek_pair(wave ? my_map() : state(super()));
+        if (wave && wave <= groups_before()) wg = peek_pair(my_group_map());
+    }
+    // (a, h) = the first n maps that the waves fetched, composed in order
+    __device__ __forceinline__ void compose(int n, const float (&A)[W][64], const float (&H)[W][64], float& a,
+                                            float& h) const {
+        a = 1.0f, h = 0.0f;
+        for (int k = 1; k <= n; ++k) {
+            h = fmaf(A[k][l], h, H[k][l]);
+            a *= A[k][l];
         }
     }
-    if (before > 0) {
-        // wave w composes its share of the maps before
-        const int per = (before + W - 1) / W;
-        const int lo = min(wave * per, before), hi = min(lo + per, before);
-        float PA[V], PH[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) PA[j] = 1.0f, PH[j] = 0.0f;
-        constexpr int kBatch = 4;  // looked at together
-        for (int k = lo; k < hi; k += kBatch) {
-            uint64_t w[kBatch][V];
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-                    w[i][j] = peek_pair(c.map_at(chain, g * c.group + min(k + i, hi - 1)) + l + j);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                if (k + i >= hi) break;
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float a, h;
-                    get_pair(c.map_at(chain, g * c.group + k + i) + l + j, w[i][j], a, h);
-                    PH[j] = fmaf(a, PH[j], h);
-                    PA[j] *= a;
-                }
+    // After that barrier; wave 0 holds the tile's own map (A, H) and the state before the chain, `first`.
+    __device__ __forceinline__ void finish(bool last, float first, float A, float H) {
+        const bool closes = tiles_before() == W - 1, closes_super = closes && groups_before() == W - 1;
+        float a, h;
+        if (wave == 0) {
+            if (!last && !closes) {
+                // the map goes out after `first` has come in: the chain's last tile, which waits for
+                // the map, may write its result where `first` was read
+                asm volatile("" : "+v"(A), "+v"(first));
+                put_pair(map(rank), A, H);
+            }
+        } else if (wave <= tiles_before()) {
+            get_pair(my_map(), wm, s.PA[wave][l], s.PH[wave][l]);
+        }
+        if (closes && !closes_super && !last) {
+            // the group's map goes out before anything outside the group is waited for
+            __syncthreads();
+            if (wave == 0) {
+                compose(W - 1, s.PA, s.PH, a, h);
+                a *= A;
+                asm volatile("" : "+v"(a), "+v"(first));
+                put_pair(group_map(group()), a, fmaf(A, h, H));
             }
         }
-#pragma unroll
-        for (int j = 0; j < V; ++j) s.PA[wave][l + j] = PA[j], s.PH[wave][l + j] = PH[j];
+        if (wave && wave <= groups_before()) get_pair(my_group_map(), wg, s.GA[wave][l], s.GH[wave][l]);
+        __syncthreads();
+        if (wave == 0) {
+            float tag, st = first, ga, gh;
+            compose(groups_before(), s.GA, s.GH, ga, gh);
+            compose(tiles_before(), s.PA, s.PH, a, h);
+            if (super() > 0) get_pair(state(super()), wm, tag, st);
+            st = fmaf(a, fmaf(ga, st, gh), h);
+            if (!last && closes_super) put_pair(state(super() + 1), 0.0f, fmaf(A, st, H));
+            s.carry[l] = st;
+        }
         __syncthreads();
     }
-    if (wave == 0) {
-        float a[V], h[V], st[V];
-        uint64_t w[V];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            a[j] = 1.0f, h[j] = 0.0f, st[j] = first[j];
-            if (g > 0) w[j] = peek_pair(c.state_at(chain, g) + l + j);
-        }
-        if (before > 0) {
-#pragma unroll 2
-            for (int k = 0; k < W; ++k)
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    h[j] = fmaf(s.PA[k][l + j], h[j], s.PH[k][l + j]);
-                    a[j] *= s.PA[k][l + j];
-                }
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float tag;
-            if (g > 0) get_pair(c.state_at(chain, g) + l + j, w[j], tag, st[j]);
-            st[j] = fmaf(a[j], st[j], h[j]);
-            if (!last && closes) put_pair(c.state_at(chain, g + 1) + l + j, 0.0f, fmaf(A[j], st[j], H[j]));
-            s.carry[l + j] = st[j];
-        }
-    }
-    __syncthreads();
-}
+};
 
-// The chain block's layout in the workspace, for blocks of `width` channels.
-__device__ inline Chain chain_of(void* ws, int chains, int tiles, int group, int width) {
+// The chains' layout in the workspace.
+__device__ inline Chain chain_of(void* ws, int chains, int tiles) {
     Chain c;
     c.tiles = tiles;
-    c.group = group;
-    c.groups = (c.tiles + group - 1) / group;
-    c.width = width;
+    c.groups = (tiles + kScanWaves - 1) / kScanWaves;
+    c.supers = (c.groups + kScanWaves - 1) / kScanWaves;
     c.maps = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kTicketBytes);
-    c.states = c.maps + static_cast<int64_t>(chains) * c.tiles * width;
+    c.group_maps = c.maps + static_cast<int64_t>(chains) * c.tiles * 64;
+    c.states = c.group_maps + static_cast<int64_t>(chains) * c.groups * 64;
     return c;
+}
+
+// What a workgroup works on: its ticket's tile and chain.
+struct Place {
+    int pos, chain, b, wave, l, c;  // pos: the tile's place in the order of tickets
+};
+__device__ __forceinline__ Place take_place(void* ws, int D, int chains, uint32_t* ticket) {
+    uint32_t id = blockIdx.x;
+    if (ws) {
+        if (threadIdx.x == 0) *ticket = atomicAdd(static_cast<uint32_t*>(ws), 1u);
+        __syncthreads();
+        id = __builtin_amdgcn_readfirstlane(*ticket);
+    }
+    Place at;
+    const int nblk = (D + 63) / 64;
+    at.pos = static_cast<int>(id / chains);
+    at.chain = static_cast<int>(id % chains);
+    at.b = at.chain / nblk;
+    at.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    at.l = threadIdx.x & 63;
+    at.c = at.chain % nblk * 64 + at.l;
+    return at;
 }
 
 }  // namespace layer

@@ -10,10 +10,12 @@
 
 namespace layer {
 
-// Tokens per tile (what a workgroup takes) of the scan's forward and backward.  A saving
-// forward keeps the state before each of the backward's tiles.
-constexpr int kFwdTile = 128;
-constexpr int kBwdTile = 64;
+// Tokens per tile (what a workgroup takes, each wave a run of them) of the scan's
+// forward and backward.  A saving forward keeps the state before each of the backward's tiles.
+constexpr int kScanWaves = 8;
+constexpr int kFwdRun = 32, kFwdTile = kFwdRun * kScanWaves;
+constexpr int kBwdRun = 16, kBwdTile = kBwdRun * kScanWaves;
+static_assert(kFwdTile % kBwdTile == 0 && kBwdTile % kFwdRun == 0, "a saved state is one before a run");
 inline int64_t tiles_of(int64_t T, int tile) { return (T + tile - 1) / tile; }
 
 // Parameters of the scan's kernels; layouts as in include/lattice_osr.h.
@@ -36,13 +38,11 @@ struct ScanParams {
     // Hand-offs between the workgroups of a chain (scan_workspace_bytes), or
     // null where T is one tile: a ticket counter, then the pairs (layer_chain.h).
     void* ws;
-    int group;      // tiles per group
 };
 
-// Bytes of ScanParams::ws and the tiles per group, for B sequences of T tokens and D channels.
+// Bytes of ScanParams::ws for B sequences of T tokens and D channels.
 size_t scan_workspace_bytes(int B, int T, int D);
-int scan_group(int B, int T, int D);
-void clear_scan_workspace(const ScanParams& p, hipStream_t st);
+void clear_scan_workspace(const ScanParams& p, int tile, hipStream_t st);
 // Return 0 or -5 (launch error).
 int launch_scan_fwd(const ScanParams& p, hipStream_t st);
 int launch_scan_bwd(const ScanParams& p, hipStream_t st);

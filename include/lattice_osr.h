@@ -435,7 +435,7 @@ LATTICE_OSR_API int lattice_osr_glue_post(const lattice_osr_desc* desc, const vo
  * mu_logit = -inf drops the state before a token (a document's border inside a
  * row), +inf keeps it; either has a zero gradient.  D up to 2^20 and T up
  * to 2^30, odd ones included; element alignment only (rows move in wider pieces
- * where D and the addresses allow).  B ceil(D / 64) ceil(T / 64) must stay
+ * where D and the addresses allow).  B ceil(D / 64) ceil(T / 128) must stay
  * below 2^22.
  */
 #define LATTICE_OSR_SCAN_ONE 0        /* w = 1                  */
@@ -456,8 +456,8 @@ typedef struct {
  * Forward.  state_out may be NULL (not wanted) or state_in itself; no other
  * output may overlap an argument (ERR_ALIAS).  saved, where not NULL, receives
  * what lattice_osr_scan_bwd needs (lattice_osr_scan_saved_bytes(desc) bytes, 4-byte
- * aligned).  workspace must hold lattice_osr_scan_workspace_bytes(desc) bytes
- * (NULL allowed where that is 0); its contents on entry are ignored, and calls
+ * aligned).  workspace must hold lattice_osr_scan_workspace_bytes(desc) bytes, 16-byte
+ * aligned (NULL allowed where that is 0); its contents on entry are ignored, and calls
  * that may overlap in time need one each.  Results do not depend on how the
  * work is split: reruns agree bit for bit.  Errors and asynchrony as above.
  */

@@ -81,10 +81,10 @@ def test_scan_step_takes_one_token():
 
 
 def test_scan_saved_size_and_bounds():
-    """One state per 64 tokens, begun ones included."""
+    """One state per 128 tokens, begun ones included."""
     for B, T, D in ((1, 1, 1), (2, 128, 64), (3, 129, 65), (1, 65536, 2048)):
         d = osr.make_scan_desc(B, T, D)
-        need = B * ((T + 63) // 64) * D * 4
+        need = B * ((T + 127) // 128) * D * 4
         assert osr.lattice_osr_scan_saved_bytes(d) == need
         assert _fwd(d, _fake(*FWD), saved_bytes=need - 1) == osr.ERR_WORKSPACE
         assert _bwd(d, _fake(*BWD), saved_bytes=need - 1) == osr.ERR_WORKSPACE
@@ -280,8 +280,8 @@ def test_norm_binding_checks():
 
 
 def test_scan_workspace():
-    """None for a single tile; required, sized, 8-byte aligned and apart from every argument otherwise."""
-    assert osr.lattice_osr_scan_workspace_bytes(osr.make_scan_desc(3, 64, 100)) == 0
+    """None for a single tile; required, sized, 16-byte aligned and apart from every argument otherwise."""
+    assert osr.lattice_osr_scan_workspace_bytes(osr.make_scan_desc(3, 128, 100)) == 0
     d = osr.make_scan_desc(3, 200, 100)
     need = osr.lattice_osr_scan_workspace_bytes(d)
     assert need > 0
@@ -289,6 +289,6 @@ def test_scan_workspace():
         p = _fake(*names)
         assert call(d, p, ws=None) == osr.ERR_NULL
         assert call(d, p, ws_bytes=need - 1) == osr.ERR_WORKSPACE
-        assert call(d, p, ws=WS + 4) == osr.ERR_ALIGN
+        assert call(d, p, ws=WS + 8) == osr.ERR_ALIGN
         for n in names:
             assert call(d, p, ws=p[n]) == osr.ERR_ALIAS, n

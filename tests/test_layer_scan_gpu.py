@@ -127,6 +127,30 @@ def test_padded_batch(D, dtype):
                 assert torch.equal(st[i], x["state_in"][i]) and torch.equal(g["dstate_in"][i], dso[i])
 
 
+def test_lengths_across_every_level():
+    """Sequences that end at, before and behind the borders of runs, tiles, groups of tiles and groups of
+    groups, in one batch, next to an empty one."""
+    T, D = 17000, 5
+    lens = [0, 1, 31, 33, 127, 129, 256, 257, 1023, 1025, 2047, 2048, 2049, 8191, 8192, 8193, 16383, 16384, 16385, T]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    x = make(len(lens), T, D, F, seed=18, mean=4.0)
+    got = run_all(x, osr.SCAN_COMPLEMENT, n)
+    for i, k in enumerate(lens):
+        for name in ("y", "dv", "dmu_logit", "dgamma_logit"):
+            assert (got[name][i, k:] == 0).all(), (name, i)
+
+
+def test_state_in_place_at_every_length():
+    """state_out is state_in: every tile that reads the old state does so before the last one writes."""
+    for T in (1, 200, 257, 700, 2100, 20000):
+        x = make(3, T, 70, BF, seed=T)
+        want = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], gamma_logit=x["gamma_logit"])
+        for _ in range(3):
+            st = x["state_in"].clone()
+            y, _ = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], st, gamma_logit=x["gamma_logit"], state_out=st)
+            assert torch.equal(y, want[0]) and torch.equal(st, want[1]), T
+
+
 def test_all_sequences_empty():
     x = make(3, 50, 40, BF)
     n = torch.zeros(3, dtype=torch.int32, device="cuda")
