@@ -2,6 +2,8 @@
 // vectors of V consecutive elements, and the gates.
 #pragma once
 
+#include <type_traits>
+
 #include "osr_device.h"
 
 namespace layer {
@@ -68,6 +70,52 @@ __device__ __forceinline__ float weight_of(float m, float om) {
     if constexpr (WT == 1) return om;
     if constexpr (WT == 2) return __builtin_amdgcn_sqrtf(om * (1.0f + m));
     return 1.0f;
+}
+
+// Some rows of a tensor as a buffer of their own: an access past the last of them, or
+// by a lane without channels (kOut), reads zero and writes nothing; so does every access
+// to one of no bytes, which stands for an absent tensor.  Offsets are in bytes, whole in the
+// address register (the part of the bounds check that needs no care); a buffer has at
+// most 2^30 of them, so kOut plus a row's offset lies outside and does not wrap.
+constexpr uint32_t kOut = 0x80000000u;
+// Streamed once, rows are loaded non-temporally (B8 T4096 D2048 bf16 forward 90 -> 83 us; inputs that
+// the 256 MB cache still holds lose: B7 T1531 D1001 fp32 36 -> 40).  The backward's stores too
+// (training step 322 -> 306 us); not the forward's, whose y the next kernel reads.
+constexpr int kNt = 2;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t first, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, bytes, 0x00020000);
+}
+template <typename T>
+__device__ __forceinline__ T load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+    if constexpr (sizeof(T) == 2)
+        return __builtin_bit_cast(T, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kNt)));
+    else
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kNt));
+}
+// NT: written past the caches.
+template <bool BF16, bool NT>
+__device__ __forceinline__ void store_row(__amdgpu_buffer_rsrc_t r, uint32_t off, float x) {
+    if constexpr (BF16)
+        __builtin_amdgcn_raw_buffer_store_b16(osr::f32_to_bf16_bits(x), r, off, 0, NT ? kNt : 0);
+    else
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), r, off, 0, NT ? kNt : 0);
+}
+
+// The value, in a register whose origin the compiler does not see: offsets taken from
+// it are formed where they are used and not held from the top of the kernel (16 to 32 registers).
+__device__ __forceinline__ uint32_t here(uint32_t x) {
+    asm("" : "+v"(x));
+    return x;
+}
+
+// f(constant) for a flag that is the same in every thread: one branch around a whole
+// loop instead of one in each of its steps.
+template <typename F>
+__device__ __forceinline__ void with_flag(bool flag, F&& f) {
+    if (flag)
+        f(std::true_type());
+    else
+        f(std::false_type());
 }
 
 }  // namespace layer

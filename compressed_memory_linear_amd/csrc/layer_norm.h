@@ -35,28 +35,50 @@ struct Piece {
     T e[kE];
 };
 
-// Piece k of a row (zeros past its end); p is the row's first value.
+// The rows that a workgroup takes at once, as one buffer per tensor (of no bytes where
+// the tensor is absent or the rows lie past the last): loads and stores need no branch.
+struct Rows {
+    int64_t first;  // element
+    int count;      // elements
+};
+template <typename S>
+__device__ __forceinline__ Rows rows_of(uint32_t it, int R, int D) {
+    const int64_t left = R - static_cast<int64_t>(it) * S::ROWS;
+    const int rows = left <= 0 ? 0 : left < S::ROWS ? static_cast<int>(left) : S::ROWS;
+    return Rows{static_cast<int64_t>(it) * S::ROWS * D, rows * D};
+}
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t norm_rsrc(const void* p, bool bf16, Rows r) {
+    const int e = bf16 ? 2 : 4;
+    return rows_rsrc(p, r.first * e, p ? r.count * e : 0);
+}
+// Byte offset of this thread's value e of piece k among those rows.
+template <typename S, bool VEC>
+__device__ __forceinline__ uint32_t off_of(int lane, int sub, int k, int e, int D, int size) {
+    const int c = col_of<S, VEC>(lane, k, e);
+    return c < D ? static_cast<uint32_t>(sub * D + c) * size : kOut;
+}
+
+typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
 template <typename S, bool VEC, typename T>
-__device__ __forceinline__ void load_piece(const T* p, int lane, int k, int D, Piece<T>& o) {
-    if (VEC) {
-        const int c = col_of<S, true>(lane, k, 0);
+__device__ __forceinline__ void load_piece(__amdgpu_buffer_rsrc_t r, int lane, int sub, int k, int D, Piece<T>& o) {
+    if constexpr (VEC) {
+        const uint32_t at = off_of<S, true>(lane, sub, k, 0, D, sizeof(T));
         constexpr int N = 16 / sizeof(T);
-        if (c < D) {
 #pragma unroll
-            for (int i = 0; i < kE / N; ++i) {
-                const Vec<T, N> v = load_vec<T, N>(p, c + i * N);
+        for (int i = 0; i < kE / N; ++i) {
+            const auto v = __builtin_bit_cast(
+                Vec<T, N>, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * 16, 0, 0));
 #pragma unroll
-                for (int j = 0; j < N; ++j) o.e[i * N + j] = v.e[j];
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) o.e[e] = T(0);
+            for (int j = 0; j < N; ++j) o.e[i * N + j] = v.e[j];
         }
     } else {
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
-            const int c = col_of<S, false>(lane, k, e);
-            o.e[e] = c < D ? p[c] : T(0);
+            const uint32_t at = off_of<S, false>(lane, sub, k, e, D, sizeof(T));
+            if constexpr (sizeof(T) == 2)
+                o.e[e] = __builtin_bit_cast(T, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0)));
+            else
+                o.e[e] = __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0));
         }
     }
 }
@@ -69,26 +91,32 @@ __device__ __forceinline__ void load_weights(const float* p, int lane, int k, in
     }
 }
 template <typename S, bool VEC>
-__device__ __forceinline__ void store_piece(void* p, bool bf16, int64_t row, int lane, int k, int D,
+__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, bool bf16, int lane, int sub, int k, int D,
                                             const float (&x)[kE]) {
-    if (VEC) {
-        const int c = col_of<S, true>(lane, k, 0);
-        if (c >= D) return;
-        if (bf16) {
-            store_vec<kE>(p, row + c, x, true);
-        } else {
-            const float lo[4] = {x[0], x[1], x[2], x[3]}, hi[4] = {x[4], x[5], x[6], x[7]};
-            store_vec<4>(p, row + c, lo, false);
-            store_vec<4>(p, row + c + 4, hi, false);
-        }
-    } else {
+    with_flag(bf16, [&](auto b) {
+        constexpr bool BF16 = decltype(b)::value;
+        constexpr int size = BF16 ? 2 : 4;
+        if constexpr (VEC) {
+            const uint32_t at = off_of<S, true>(lane, sub, k, 0, D, size);
+            if constexpr (BF16) {
+                u32x4_t w;
 #pragma unroll
-        for (int e = 0; e < kE; ++e) {
-            const int c = col_of<S, false>(lane, k, e);
-            const float v[1] = {x[e]};
-            if (c < D) store_vec<1>(p, row + c, v, bf16);
+                for (int j = 0; j < 4; ++j)
+                    w[j] = osr::f32_to_bf16_bits(x[2 * j]) |
+                           static_cast<uint32_t>(osr::f32_to_bf16_bits(x[2 * j + 1])) << 16;
+                __builtin_amdgcn_raw_buffer_store_b128(w, r, at, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    __builtin_amdgcn_raw_buffer_store_b128(
+                        u32x4_t{__float_as_uint(x[4 * i]), __float_as_uint(x[4 * i + 1]),
+                                __float_as_uint(x[4 * i + 2]), __float_as_uint(x[4 * i + 3])}, r, at + 16 * i, 0, 0);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kE; ++e) store_row<BF16, false>(r, off_of<S, false>(lane, sub, k, e, D, size), x[e]);
         }
-    }
+    });
 }
 
 // Sums of N values over the threads of a row, in all of them, in a fixed order.  Across
@@ -125,6 +153,27 @@ struct RowSum {
 __device__ __forceinline__ float rsqrt_acc(float x) {
     const float r = __builtin_amdgcn_rsqf(x);
     return r > 0.0f ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
+}
+
+// GeLU's parts for a gate g: cdf = Phi(g), and e = exp(-g^2 / 2), which its density takes too.
+// With a = |g| and t = 1 / (1 + 0.35 a), Phi(-a) = e t q(t): q is the polynomial of degree 8
+// nearest to exp(a^2 / 2) Phi(-a) / t in relative error (1.6e-7 over all a, fitted for this by
+// reweighted least squares), so the lower tail keeps its relative accuracy; the argument
+// of the exponential, rounded, costs up to g^2 2^-24.  A third of the operations of erfcf.
+__device__ __forceinline__ void gelu_parts(float g, float& cdf, float& e) {
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.35f, fabsf(g), 1.0f));
+    e = __builtin_amdgcn_exp2f(g * g * -0.72134752f);
+    float q = -2.508340625e-02f;
+    q = fmaf(q, t, 1.262319635e-01f);
+    q = fmaf(q, t, -2.233420272e-01f);
+    q = fmaf(q, t, 1.271268000e-01f);
+    q = fmaf(q, t, -4.416478743e-03f);
+    q = fmaf(q, t, 9.897989587e-02f);
+    q = fmaf(q, t, 1.211549029e-01f);
+    q = fmaf(q, t, 1.397210148e-01f);
+    q = fmaf(q, t, 1.396274145e-01f);
+    const float lower = q * t * e;
+    cdf = g < 0.0f ? lower : 1.0f - lower;
 }
 
 // Calls f with the NormShape for rows of D values: the fewest threads that hold

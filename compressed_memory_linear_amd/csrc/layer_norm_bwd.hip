@@ -35,42 +35,56 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
 #pragma unroll
         for (int e = 0; e < kE; ++e) gpost[k][e] = gsc[k][e] = gpre[k][e] = 0.0f;
     }
-    const int steps = (p.R + S::ROWS - 1) / S::ROWS;
-    for (int it = blockIdx.x; it < steps; it += gridDim.x) {
-        const int row = it * S::ROWS + sub;
-        const bool live = row < p.R;  // past the end: a row of zeros, in step with the barriers
-        const int64_t at = static_cast<int64_t>(row) * p.D;
+    struct Raw {
+        Piece<TIn> y, g, z;
+        Piece<TRes> x, d;
+    };
+    auto fetch = [&](uint32_t it, Raw (&o)[S::K]) {
+        const Rows rows = rows_of<S>(it, p.R, p.D);
+        const auto yr = norm_rsrc(p.y, sizeof(TIn) == 2, rows), gr = norm_rsrc(p.gate, sizeof(TIn) == 2, rows);
+        const auto zr = norm_rsrc(p.dz, sizeof(TIn) == 2, rows), xr = norm_rsrc(p.x, sizeof(TRes) == 2, rows);
+        const auto dr = norm_rsrc(p.dx_out, sizeof(TRes) == 2, rows);
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            load_piece<S, VEC>(yr, lane, sub, k, p.D, o[k].y);
+            load_piece<S, VEC>(gr, lane, sub, k, p.D, o[k].g);
+            load_piece<S, VEC>(xr, lane, sub, k, p.D, o[k].x);
+            load_piece<S, VEC>(zr, lane, sub, k, p.D, o[k].z);
+            load_piece<S, VEC>(dr, lane, sub, k, p.D, o[k].d);
+        }
+    };
+    const uint32_t steps = (static_cast<uint32_t>(p.R) + S::ROWS - 1) / S::ROWS;
+    Raw next[S::K];
+    fetch(blockIdx.x, next);
+    for (uint32_t it = blockIdx.x; it < steps; it += gridDim.x) {
+        // rows past the last are rows of zeros, in step with the barriers
+        const Rows rows = rows_of<S>(it, p.R, p.D);
         float yv[S::K][kE], phi[S::K][kE], dphi[S::K][kE], xo[S::K][kE], d[S::K][kE], t[S::K][kE];
         float ss[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < S::K; ++k) {
-            Piece<TIn> ry = {}, rg = {}, rz = {};
-            Piece<TRes> rx = {}, rd = {};
-            if (live && p.y) load_piece<S, VEC>(static_cast<const TIn*>(p.y) + at, lane, k, p.D, ry);
-            if (live && p.gate) load_piece<S, VEC>(static_cast<const TIn*>(p.gate) + at, lane, k, p.D, rg);
-            if (live && p.x) load_piece<S, VEC>(static_cast<const TRes*>(p.x) + at, lane, k, p.D, rx);
-            if (live && p.dx_out) load_piece<S, VEC>(static_cast<const TRes*>(p.dx_out) + at, lane, k, p.D, rd);
-            if (live && p.dz) load_piece<S, VEC>(static_cast<const TIn*>(p.dz) + at, lane, k, p.D, rz);
+            const Raw raw = next[k];
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-                yv[k][e] = widen(ry.e[e]);
-                xo[k][e] = widen(rx.e[e]);
-                d[k][e] = widen(rd.e[e]);
-                t[k][e] = widen(rz.e[e]);
+                yv[k][e] = widen(raw.y.e[e]);
+                xo[k][e] = widen(raw.x.e[e]);
+                d[k][e] = widen(raw.d.e[e]);
+                t[k][e] = widen(raw.z.e[e]);
                 phi[k][e] = 1.0f, dphi[k][e] = 0.0f;
             }
             if (p.gate_kind == 1) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
-                    const float g = widen(rg.e[e]);
-                    const float cdf = 0.5f * erfcf(-g * 0.70710678118654752f);
+                    const float g = widen(raw.g.e[e]);
+                    float cdf, ex;
+                    gelu_parts(g, cdf, ex);
                     phi[k][e] = g * cdf;
-                    dphi[k][e] = fmaf(g * 0.39894228040143268f, exp_of<true>(-0.5f * g * g), cdf);
+                    dphi[k][e] = fmaf(g * 0.39894228040143268f, ex, cdf);
                 }
             } else if (p.gate_kind == 2) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
-                    const float g = widen(rg.e[e]);
+                    const float g = widen(raw.g.e[e]);
                     float s, r;
                     sigmoid2<true>(g, s, r);
                     phi[k][e] = g * s;
@@ -83,6 +97,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
                 ss[0] = fmaf(u, u, ss[0]);
             }
         }
+        fetch(it + gridDim.x, next);  // in flight while this row is worked on
         float r1 = 1.0f;
         if (p.y) {
             if (p.post) {
@@ -116,10 +131,9 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
                     d[k][e] = fmaf(r2, fmaf(-xh, m, t[k][e] * wpre[k][e]), d[k][e]);
                 }
         }
-        if (p.dx && live) {
+        const auto dxr = norm_rsrc(p.dx, p.res_bf16, rows);
 #pragma unroll
-            for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(p.dx, p.res_bf16, at, lane, k, p.D, d[k]);
-        }
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(dxr, p.res_bf16, lane, sub, k, p.D, d[k]);
         if (!p.y) continue;
         ss[0] = ss[1] = 0.0f;
 #pragma unroll
@@ -141,16 +155,17 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) d[k][e] = r1 * fmaf(-(yv[k][e] * phi[k][e] * r1), m, d[k][e]);
         }
+        const auto dyr = norm_rsrc(p.dy, p.grad_bf16, rows), dgr = norm_rsrc(p.dgate, p.grad_bf16, rows);
 #pragma unroll
         for (int k = 0; k < S::K; ++k) {
             float o[kE];
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[e] = d[k][e] * phi[k][e];
-            if (live) store_piece<S, VEC>(p.dy, p.grad_bf16, at, lane, k, p.D, o);
+            store_piece<S, VEC>(dyr, p.grad_bf16, lane, sub, k, p.D, o);
             if (p.dgate) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) o[e] = d[k][e] * yv[k][e] * dphi[k][e];
-                if (live) store_piece<S, VEC>(p.dgate, p.grad_bf16, at, lane, k, p.D, o);
+                store_piece<S, VEC>(dgr, p.grad_bf16, lane, sub, k, p.D, o);
             }
         }
     }

@@ -23,32 +23,49 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
         load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
         load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
     }
-    const int steps = (p.R + S::ROWS - 1) / S::ROWS;
-    for (int it = blockIdx.x; it < steps; it += gridDim.x) {
-        const int row = it * S::ROWS + sub;
-        const bool live = row < p.R;  // past the end: a row of zeros, in step with the barriers
-        const int64_t at = static_cast<int64_t>(row) * p.D;
+    struct Raw {
+        Piece<TIn> y, g;
+        Piece<TRes> x;
+    };
+    auto fetch = [&](uint32_t it, Raw (&o)[S::K]) {
+        const Rows rows = rows_of<S>(it, p.R, p.D);
+        const auto yr = norm_rsrc(p.y, sizeof(TIn) == 2, rows), gr = norm_rsrc(p.gate, sizeof(TIn) == 2, rows);
+        const auto xr = norm_rsrc(p.x, sizeof(TRes) == 2, rows);
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            load_piece<S, VEC>(yr, lane, sub, k, p.D, o[k].y);
+            load_piece<S, VEC>(gr, lane, sub, k, p.D, o[k].g);
+            load_piece<S, VEC>(xr, lane, sub, k, p.D, o[k].x);
+        }
+    };
+    const uint32_t steps = (static_cast<uint32_t>(p.R) + S::ROWS - 1) / S::ROWS;
+    Raw next[S::K];
+    fetch(blockIdx.x, next);
+    for (uint32_t it = blockIdx.x; it < steps; it += gridDim.x) {
+        // rows past the last are rows of zeros, in step with the barriers
+        const Rows rows = rows_of<S>(it, p.R, p.D);
         float u[S::K][kE], xo[S::K][kE];
         float ss[1] = {0.0f};
 #pragma unroll
         for (int k = 0; k < S::K; ++k) {
-            Piece<TIn> ry = {}, rg = {};
-            Piece<TRes> rx = {};
-            if (live && p.y) load_piece<S, VEC>(static_cast<const TIn*>(p.y) + at, lane, k, p.D, ry);
-            if (live && p.gate) load_piece<S, VEC>(static_cast<const TIn*>(p.gate) + at, lane, k, p.D, rg);
-            if (live && p.x) load_piece<S, VEC>(static_cast<const TRes*>(p.x) + at, lane, k, p.D, rx);
+            const Raw raw = next[k];
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
-                u[k][e] = widen(ry.e[e]);
-                xo[k][e] = widen(rx.e[e]);
+                u[k][e] = widen(raw.y.e[e]);
+                xo[k][e] = widen(raw.x.e[e]);
             }
             if (p.gate_kind == 1) {
 #pragma unroll
-                for (int e = 0; e < kE; ++e) u[k][e] *= osr::gelu(widen(rg.e[e]));
+                for (int e = 0; e < kE; ++e) {
+                    const float g = widen(raw.g.e[e]);
+                    float cdf, ex;
+                    gelu_parts(g, cdf, ex);
+                    u[k][e] *= g * cdf;
+                }
             } else if (p.gate_kind == 2) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) {
-                    const float g = widen(rg.e[e]);
+                    const float g = widen(raw.g.e[e]);
                     float s, r;
                     sigmoid2<true>(g, s, r);
                     u[k][e] *= g * s;
@@ -57,6 +74,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
 #pragma unroll
             for (int e = 0; e < kE; ++e) ss[0] = fmaf(u[k][e], u[k][e], ss[0]);
         }
+        fetch(it + gridDim.x, next);  // in flight while this row is worked on
         if (p.y) {
             float r1 = 1.0f;
             if (p.post) {
@@ -68,10 +86,9 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) xo[k][e] = fmaf(u[k][e] * r1 * wpost[k][e], sc[k][e], xo[k][e]);
         }
-        if (p.x_out && live) {
+        const auto out = norm_rsrc(p.x_out, p.res_bf16, rows);
 #pragma unroll
-            for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(p.x_out, p.res_bf16, at, lane, k, p.D, xo[k]);
-        }
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(out, p.res_bf16, lane, sub, k, p.D, xo[k]);
         if (p.pre) {
             ss[0] = 0.0f;
 #pragma unroll
@@ -80,11 +97,12 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
                 for (int e = 0; e < kE; ++e) ss[0] = fmaf(xo[k][e], xo[k][e], ss[0]);
             sum(ss);
             const float r2 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+            const auto zr = norm_rsrc(p.z, p.in_bf16, rows);
 #pragma unroll
             for (int k = 0; k < S::K; ++k) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) xo[k][e] *= r2 * wpre[k][e];
-                if (live) store_piece<S, VEC>(p.z, p.in_bf16, at, lane, k, p.D, xo[k]);
+                store_piece<S, VEC>(zr, p.in_bf16, lane, sub, k, p.D, xo[k]);
             }
         }
     }
@@ -106,7 +124,7 @@ void launch(const NormParams& p, hipStream_t st) {
 int norm_groups(int R, int D, bool backward) {
     int rows = 1, nt = 256;
     with_shape(D, [&](auto s) { rows = decltype(s)::ROWS, nt = decltype(s)::NT; });
-    const int steps = (R + rows - 1) / rows;
+    const int steps = static_cast<int>((static_cast<int64_t>(R) + rows - 1) / rows);
     const int most = (backward ? 512 : 1024) * 256 / nt;
     return steps < most ? steps : most;
 }
