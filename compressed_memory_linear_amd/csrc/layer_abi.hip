@@ -102,7 +102,7 @@ layer::NormParams norm_params(const lattice_osr_norm_desc* d, bool backward) {
     return p;
 }
 
-// Whether the rows can move in 16-byte pieces.
+// Whether the rows and weights can move in 16-byte pieces.
 bool norm_vec(const lattice_osr_norm_desc* d, const Buf* b, int n) {
     if (d->D % 8 != 0) return false;
     for (int i = 0; i < n; ++i)
@@ -239,7 +239,7 @@ int lattice_osr_norm_fwd(const lattice_osr_norm_desc* desc, const void* y, const
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
     layer::NormParams p = norm_params(desc, false);
-    p.vec = norm_vec(desc, bufs, 5);
+    p.vec = norm_vec(desc, bufs, 8);
     p.y = y, p.gate = gate, p.x = x;
     p.w_post = w_post, p.scale = scale, p.w_pre = w_pre;
     p.x_out = x_out, p.z = z;
@@ -283,7 +283,7 @@ int lattice_osr_norm_bwd(const lattice_osr_norm_desc* desc, const void* y, const
     rc = check_buffers(bufs, sizeof(bufs) / sizeof(bufs[0]));
     if (rc != LATTICE_OSR_OK) return rc;
     layer::NormParams p = norm_params(desc, true);
-    p.vec = norm_vec(desc, bufs, 8);
+    p.vec = norm_vec(desc, bufs, 11);
     p.y = y, p.gate = gate, p.x = x;
     p.w_post = w_post, p.scale = scale, p.w_pre = w_pre;
     p.dx_out = dx_out, p.dz = dz;

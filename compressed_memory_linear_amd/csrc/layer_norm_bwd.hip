@@ -25,16 +25,6 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     const int sub = threadIdx.x / S::TPR;
     const float inv = 1.0f / static_cast<float>(p.D);
 
-    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
-    float gpost[S::K][kE], gsc[S::K][kE], gpre[S::K][kE];
-#pragma unroll
-    for (int k = 0; k < S::K; ++k) {
-        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
-        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
-        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
-#pragma unroll
-        for (int e = 0; e < kE; ++e) gpost[k][e] = gsc[k][e] = gpre[k][e] = 0.0f;
-    }
     struct Raw {
         Piece<TIn> y, g, z;
         Piece<TRes> x, d;
@@ -56,6 +46,16 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     const uint32_t steps = (static_cast<uint32_t>(p.R) + S::ROWS - 1) / S::ROWS;
     Raw next[S::K];
     fetch(blockIdx.x, next);
+    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
+    float gpost[S::K][kE], gsc[S::K][kE], gpre[S::K][kE];
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
+        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
+        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) gpost[k][e] = gsc[k][e] = gpre[k][e] = 0.0f;
+    }
     for (uint32_t it = blockIdx.x; it < steps; it += gridDim.x) {
         // rows past the last are rows of zeros, in step with the barriers
         const Rows rows = rows_of<S>(it, p.R, p.D);
@@ -86,7 +86,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
                 for (int e = 0; e < kE; ++e) {
                     const float g = widen(raw.g.e[e]);
                     float s, r;
-                    sigmoid2<true>(g, s, r);
+                    sigmoid2<kAccurate<TIn>>(g, s, r);
                     phi[k][e] = g * s;
                     dphi[k][e] = s * fmaf(g, r, 1.0f);
                 }
@@ -133,7 +133,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
         }
         const auto dxr = norm_rsrc(p.dx, p.res_bf16, rows);
 #pragma unroll
-        for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(dxr, p.res_bf16, lane, sub, k, p.D, d[k]);
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC, true>(dxr, p.res_bf16, lane, sub, k, p.D, d[k]);
         if (!p.y) continue;
         ss[0] = ss[1] = 0.0f;
 #pragma unroll
@@ -161,11 +161,11 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
             float o[kE];
 #pragma unroll
             for (int e = 0; e < kE; ++e) o[e] = d[k][e] * phi[k][e];
-            store_piece<S, VEC>(dyr, p.grad_bf16, lane, sub, k, p.D, o);
+            store_piece<S, VEC, true>(dyr, p.grad_bf16, lane, sub, k, p.D, o);
             if (p.dgate) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) o[e] = d[k][e] * yv[k][e] * dphi[k][e];
-                store_piece<S, VEC>(dgr, p.grad_bf16, lane, sub, k, p.D, o);
+                store_piece<S, VEC, true>(dgr, p.grad_bf16, lane, sub, k, p.D, o);
             }
         }
     }
@@ -197,26 +197,26 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     if (p.dw_pre) put(part + 2 * p.D, gpre);
 }
 
-// out[c] = sum over the workgroups of part[g][which][c]: 64 columns and 16 rows of
-// threads to a workgroup, each adding every 16th row in order.
+// out[c] = sum over the workgroups of part[g][which][c]: 32 columns and 32 rows of
+// threads to a workgroup, each adding every 32nd row in order.
 __global__ __launch_bounds__(1024) void layer_norm_cols_kernel(NormParams p) {
-    __shared__ float s[16][64];
+    __shared__ float s[32][33];
     const int which = blockIdx.y;
     float* out = which == 0 ? p.dw_post : which == 1 ? p.dscale : p.dw_pre;
     if (!out) return;
-    const int l = threadIdx.x & 63, r = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + l;
+    const int l = threadIdx.x & 31, r = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + l;
     float a = 0.0f;
     if (c < p.D) {
-#pragma unroll 8
-        for (int g = r; g < p.groups; g += 16) a += p.part[(static_cast<int64_t>(g) * 3 + which) * p.D + c];
+#pragma unroll 16
+        for (int g = r; g < p.groups; g += 32) a += p.part[(static_cast<int64_t>(g) * 3 + which) * p.D + c];
     }
     s[r][l] = a;
     __syncthreads();
     if (r == 0 && c < p.D) {
         float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t += s[i][l];
+        for (int i = 0; i < 32; ++i) t += s[i][l];
         out[c] = t;
     }
 }
@@ -240,7 +240,7 @@ int launch_norm_bwd(const NormParams& p, hipStream_t st) {
     else
         p.res_bf16 ? launch<float, uint16_t>(p, st) : launch<float, float>(p, st);
     if (p.dw_post || p.dscale || p.dw_pre)
-        hipLaunchKernelGGL(layer_norm_cols_kernel, dim3((p.D + 63) / 64, 3), dim3(1024), 0, st, p);
+        hipLaunchKernelGGL(layer_norm_cols_kernel, dim3((p.D + 31) / 32, 3), dim3(1024), 0, st, p);
     return hipGetLastError() == hipSuccess ? 0 : -5;
 }
 

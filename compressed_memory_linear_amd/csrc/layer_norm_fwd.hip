@@ -16,13 +16,6 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
     const int sub = threadIdx.x / S::TPR;
     const float inv = 1.0f / static_cast<float>(p.D);
 
-    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
-#pragma unroll
-    for (int k = 0; k < S::K; ++k) {
-        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
-        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
-        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
-    }
     struct Raw {
         Piece<TIn> y, g;
         Piece<TRes> x;
@@ -41,6 +34,13 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
     const uint32_t steps = (static_cast<uint32_t>(p.R) + S::ROWS - 1) / S::ROWS;
     Raw next[S::K];
     fetch(blockIdx.x, next);
+    float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        load_weights<S, VEC>(p.w_post, lane, k, p.D, wpost[k]);
+        load_weights<S, VEC>(p.scale, lane, k, p.D, sc[k]);
+        load_weights<S, VEC>(p.w_pre, lane, k, p.D, wpre[k]);
+    }
     for (uint32_t it = blockIdx.x; it < steps; it += gridDim.x) {
         // rows past the last are rows of zeros, in step with the barriers
         const Rows rows = rows_of<S>(it, p.R, p.D);
@@ -67,7 +67,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
                 for (int e = 0; e < kE; ++e) {
                     const float g = widen(raw.g.e[e]);
                     float s, r;
-                    sigmoid2<true>(g, s, r);
+                    sigmoid2<kAccurate<TIn>>(g, s, r);
                     u[k][e] *= g * s;
                 }
             }
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
         }
         const auto out = norm_rsrc(p.x_out, p.res_bf16, rows);
 #pragma unroll
-        for (int k = 0; k < S::K; ++k) store_piece<S, VEC>(out, p.res_bf16, lane, sub, k, p.D, xo[k]);
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC, false>(out, p.res_bf16, lane, sub, k, p.D, xo[k]);
         if (p.pre) {
             ss[0] = 0.0f;
 #pragma unroll
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
             for (int k = 0; k < S::K; ++k) {
 #pragma unroll
                 for (int e = 0; e < kE; ++e) xo[k][e] *= r2 * wpre[k][e];
-                store_piece<S, VEC>(zr, p.in_bf16, lane, sub, k, p.D, xo[k]);
+                store_piece<S, VEC, false>(zr, p.in_bf16, lane, sub, k, p.D, xo[k]);
             }
         }
     }
