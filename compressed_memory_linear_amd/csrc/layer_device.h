@@ -108,6 +108,14 @@ __device__ __forceinline__ uint32_t here(uint32_t x) {
     return x;
 }
 
+// The same, anew each time it is reached: what is read or computed from the result is
+// not kept from the last time.
+template <typename T>
+__device__ __forceinline__ T anew(T x) {
+    asm volatile("" : "+v"(x));
+    return x;
+}
+
 // f(constant) for a flag that is the same in every thread: one branch around a whole
 // loop instead of one in each of its steps.
 template <typename F>

@@ -16,10 +16,11 @@ namespace layer {
 constexpr int kE = 8;  // values per thread and piece
 
 // Rows are loaded non-temporally, and the backward's gradients stored so (R32768 D2048 bf16:
-// forward 128 -> 114 us from the loads, backward 212 -> 206 from the stores; the forward's stores,
-// which the next kernel reads, stay).  Each workgroup walks over its rows with the
-// next one in flight: 4 workgroups of 256 threads per compute unit in the forward, 2 in the
-// backward measured best (forward 2: 125 us, 4: 112, 6: 111; backward 1: 288, 2: 206, 3: 226, 4: 254).
+// backward 212 -> 206 us).  In the forward so is x_out, which is read again only after the next block, and
+// not z, which the next kernel reads (both plain 130 us, both non-temporal 125, so 115).  Each
+// workgroup walks over its rows with the next one in flight: 3 workgroups of 256 threads per
+// compute unit in the forward and 2 in the backward measured best (forward 2: 115 us, 3: 113, 4: 115;
+// backward 1: 288, 2: 206, 3: 226, 4: 254).
 template <int TPR_, int K_>
 struct NormShape {
     static constexpr int TPR = TPR_;                       // threads per row
@@ -125,14 +126,16 @@ __device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, bool bf16,
     });
 }
 
-// Sums of N values over the threads of a row, in all of them, in a fixed order.  Across
+// Sums of up to 2 values over the threads of a row, in all of them, in a fixed order.  Across
 // waves they meet in LDS: `buf` is used in turns of two, so that one barrier
 // separates a read from the write two sums later.
-template <typename S, int N>
+template <typename S>
 struct RowSum {
-    float (*buf)[S::NT / 64][N];  // [2][waves][N]
+    float (*buf)[S::NT / 64][2];  // [2][waves][2]
     int turn = 0;
+    template <int N>
     __device__ __forceinline__ void operator()(float (&x)[N]) {
+        static_assert(N <= 2, "the buffer's width");
 #pragma unroll
         for (int n = 0; n < N; ++n) x[n] = osr::group_sum<(S::TPR < 64 ? S::TPR : 64)>(x[n]);
         if (S::WPR == 1) return;

@@ -15,12 +15,83 @@
 namespace layer {
 namespace {
 
+// A row's five inputs, as stored.
+template <typename TIn, typename TRes>
+struct Raw {
+    Piece<TIn> y, g, z;
+    Piece<TRes> x, d;
+};
+template <typename S, bool VEC, typename TIn, typename TRes>
+__device__ __forceinline__ void fetch(const NormParams& p, uint32_t it, int lane, int sub, Raw<TIn, TRes> (&o)[S::K]) {
+    const Rows rows = rows_of<S>(it, p.R, p.D);
+    const auto yr = norm_rsrc(p.y, sizeof(TIn) == 2, rows), gr = norm_rsrc(p.gate, sizeof(TIn) == 2, rows);
+    const auto zr = norm_rsrc(p.dz, sizeof(TIn) == 2, rows), xr = norm_rsrc(p.x, sizeof(TRes) == 2, rows);
+    const auto dr = norm_rsrc(p.dx_out, sizeof(TRes) == 2, rows);
+#pragma unroll
+    for (int k = 0; k < S::K; ++k) {
+        load_piece<S, VEC>(yr, lane, sub, k, p.D, o[k].y);
+        load_piece<S, VEC>(gr, lane, sub, k, p.D, o[k].g);
+        load_piece<S, VEC>(xr, lane, sub, k, p.D, o[k].x);
+        load_piece<S, VEC>(zr, lane, sub, k, p.D, o[k].z);
+        load_piece<S, VEC>(dr, lane, sub, k, p.D, o[k].d);
+    }
+}
+// phi and phi' of a piece's gates.
+template <typename TIn>
+__device__ __forceinline__ void gates(int kind, const Piece<TIn>& raw, float (&phi)[kE], float (&dphi)[kE]) {
+#pragma unroll
+    for (int e = 0; e < kE; ++e) phi[e] = 1.0f, dphi[e] = 0.0f;
+    if (kind == 1) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const float g = widen(raw.e[e]);
+            float cdf, ex;
+            gelu_parts(g, cdf, ex);
+            phi[e] = g * cdf;
+            dphi[e] = fmaf(g * 0.39894228040143268f, ex, cdf);
+        }
+    } else if (kind == 2) {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const float g = widen(raw.e[e]);
+            float s, r;
+            sigmoid2<kAccurate<TIn>>(g, s, r);
+            phi[e] = g * s;
+            dphi[e] = s * fmaf(g, r, 1.0f);
+        }
+    }
+}
+// This workgroup's column sums g, into its row of the workspace.
+template <typename S, bool VEC>
+__device__ __forceinline__ void put_columns(float* to, float* cols, int lane, int sub, int D, const float (&g)[S::K][kE]) {
+    if constexpr (S::ROWS == 1) {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const int c = col_of<S, VEC>(lane, k, e);
+                if (c < D) to[c] = g[k][e];
+            }
+    } else {
+        constexpr int kCols = S::TPR * kE;  // the row slots' sums meet in LDS
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kE; ++e) cols[sub * kCols + col_of<S, VEC>(lane, 0, e)] = g[0][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < D; c += S::NT) {
+            float s = 0.0f;
+            for (int i = 0; i < S::ROWS; ++i) s += cols[i * kCols + c];
+            to[c] = s;
+        }
+    }
+}
+
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     __shared__ float red[2][S::NT / 64][2];
     // column sums of the workgroup's row slots (S::ROWS > 1 only)
     __shared__ float cols[S::ROWS > 1 ? S::ROWS : 1][S::ROWS > 1 ? S::TPR * kE : 1];
-    RowSum<S, 2> sum{red};
+    RowSum<S> sum{red};
     const int lane = threadIdx.x % S::TPR;
     const int sub = threadIdx.x / S::TPR;
     const float inv = 1.0f / static_cast<float>(p.D);
@@ -197,6 +268,145 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     if (p.dw_pre) put(part + 2 * p.D, gpre);
 }
 
+// The same for wide rows, on 1024 threads of 128 registers each: the weights lie in LDS, every
+// thread's own where it alone finds them (with two pieces a thread, where they do not
+// fit, they are read from the cache and no row is loaded ahead), and the gates are taken twice.
+template <typename S, bool VEC, typename TIn, typename TRes>
+__global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p) {
+    constexpr bool kAhead = S::K == 1;
+    __shared__ float red[2][S::NT / 64][2];
+    __shared__ float4 mine[kAhead ? 3 : 1][2][kAhead ? S::NT : 1];
+    RowSum<S> sum{red};
+    const int lane = threadIdx.x;
+    const float inv = 1.0f / static_cast<float>(p.D);
+    float gpost[S::K][kE] = {}, gsc[S::K][kE] = {}, gpre[S::K][kE] = {};
+    Raw<TIn, TRes> next[S::K];
+    if (kAhead) {
+        fetch<S, VEC>(p, blockIdx.x, lane, 0, next);
+        for (int n = 0; n < 3; ++n) {
+            float v[kE];
+            load_weights<S, VEC>(n == 0 ? p.w_post : n == 1 ? p.scale : p.w_pre, lane, 0, p.D, v);
+            mine[n][0][lane] = make_float4(v[0], v[1], v[2], v[3]);
+            mine[n][1][lane] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    }
+    auto weights = [&](int n, const float* from, int k, float (&o)[kE]) {
+        if constexpr (kAhead) {
+            const int t = anew(lane);
+            const float4 a = mine[n][0][t], b = mine[n][1][t];
+            o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w, o[4] = b.x, o[5] = b.y, o[6] = b.z, o[7] = b.w;
+        } else {
+            load_weights<S, VEC>(from, anew(lane), k, p.D, o);
+        }
+    };
+    for (uint32_t it = blockIdx.x; it < static_cast<uint32_t>(p.R); it += gridDim.x) {
+        const Rows rows = rows_of<S>(it, p.R, p.D);
+        Raw<TIn, TRes> raw[S::K];
+        if (!kAhead) fetch<S, VEC>(p, it, lane, 0, next);
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) raw[k] = next[k];
+        if (kAhead) fetch<S, VEC>(p, it + gridDim.x, lane, 0, next);
+        float u[S::K][kE], d[S::K][kE];
+        float ss[1] = {0.0f};
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            float phi[kE], dphi[kE];
+            gates(p.gate_kind, raw[k].g, phi, dphi);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                u[k][e] = widen(raw[k].y.e[e]) * phi[e];
+                ss[0] = fmaf(u[k][e], u[k][e], ss[0]);
+            }
+        }
+        float r1 = 1.0f;
+        if (p.y && p.post) {
+            sum(ss);
+            r1 = rsqrt_acc(fmaf(ss[0], inv, p.eps));
+        }
+        if (p.pre) {
+            float xs[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                float wp[kE], sc[kE], wq[kE];
+                weights(0, p.w_post, k, wp);
+                weights(1, p.scale, k, sc);
+                weights(2, p.w_pre, k, wq);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    d[k][e] = fmaf(u[k][e] * r1 * wp[e], sc[e], widen(raw[k].x.e[e]));  // x'
+                    xs[0] = fmaf(d[k][e], d[k][e], xs[0]);
+                    xs[1] = fmaf(widen(raw[k].z.e[e]) * wq[e], d[k][e], xs[1]);
+                }
+            }
+            sum(xs);
+            const float r2 = rsqrt_acc(fmaf(xs[0], inv, p.eps));
+            const float m = xs[1] * inv * r2;  // mean(t xh)
+#pragma unroll
+            for (int k = 0; k < S::K; ++k) {
+                float wq[kE];
+                weights(2, p.w_pre, k, wq);
+#pragma unroll
+                for (int e = 0; e < kE; ++e) {
+                    const float xh = d[k][e] * r2, z = widen(raw[k].z.e[e]);
+                    gpre[k][e] = fmaf(z, xh, gpre[k][e]);
+                    d[k][e] = fmaf(r2, fmaf(-xh, m, z * wq[e]), widen(raw[k].d.e[e]));
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) d[k][e] = widen(raw[k].d.e[e]);
+        }
+        const auto dxr = norm_rsrc(p.dx, p.res_bf16, rows);
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC, true>(dxr, p.res_bf16, lane, 0, k, p.D, d[k]);
+        if (!p.y) continue;
+        ss[0] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            float wp[kE], sc[kE];
+            weights(0, p.w_post, k, wp);
+            weights(1, p.scale, k, sc);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                u[k][e] *= r1;  // n1
+                gsc[k][e] = fmaf(d[k][e], u[k][e] * wp[e], gsc[k][e]);
+                d[k][e] *= sc[e];
+                gpost[k][e] = fmaf(d[k][e], u[k][e], gpost[k][e]);
+                d[k][e] *= wp[e];
+                ss[0] = fmaf(d[k][e], u[k][e], ss[0]);
+            }
+        }
+        if (p.post) {
+            sum(ss);
+            const float m = ss[0] * inv;  // mean(s n1)
+#pragma unroll
+            for (int k = 0; k < S::K; ++k)
+#pragma unroll
+                for (int e = 0; e < kE; ++e) d[k][e] = r1 * fmaf(-u[k][e], m, d[k][e]);
+        }
+        const auto dyr = norm_rsrc(p.dy, p.grad_bf16, rows), dgr = norm_rsrc(p.dgate, p.grad_bf16, rows);
+#pragma unroll
+        for (int k = 0; k < S::K; ++k) {
+            float phi[kE], dphi[kE], o[kE];
+#pragma unroll
+            for (int e = 0; e < kE; ++e) raw[k].g.e[e] = anew(raw[k].g.e[e]);
+            gates(p.gate_kind, raw[k].g, phi, dphi);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] = d[k][e] * phi[e];
+            store_piece<S, VEC, true>(dyr, p.grad_bf16, lane, 0, k, p.D, o);
+#pragma unroll
+            for (int e = 0; e < kE; ++e) o[e] = d[k][e] * widen(raw[k].y.e[e]) * dphi[e];
+            store_piece<S, VEC, true>(dgr, p.grad_bf16, lane, 0, k, p.D, o);
+        }
+    }
+    float* part = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.D;
+    if (p.dw_post) put_columns<S, VEC>(part, nullptr, lane, 0, p.D, gpost);
+    if (p.dscale) put_columns<S, VEC>(part + p.D, nullptr, lane, 0, p.D, gsc);
+    if (p.dw_pre) put_columns<S, VEC>(part + 2 * p.D, nullptr, lane, 0, p.D, gpre);
+}
+
 // out[c] = sum over the workgroups of part[g][which][c]: 32 columns and 32 rows of
 // threads to a workgroup, each adding every 32nd row in order.
 __global__ __launch_bounds__(1024) void layer_norm_cols_kernel(NormParams p) {
@@ -225,10 +435,14 @@ template <typename TIn, typename TRes>
 void launch(const NormParams& p, hipStream_t st) {
     with_shape(p.D, [&](auto s) {
         using S = decltype(s);
-        if (p.vec)
-            hipLaunchKernelGGL((layer_norm_bwd_kernel<S, true, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
-        else
-            hipLaunchKernelGGL((layer_norm_bwd_kernel<S, false, TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+        auto go = [&](auto vec) {
+            if constexpr (S::NT < 1024)
+                hipLaunchKernelGGL((layer_norm_bwd_kernel<S, vec(), TIn, TRes>), dim3(p.groups), dim3(S::NT), 0, st, p);
+            else
+                hipLaunchKernelGGL((layer_norm_bwd_wide_kernel<S, vec(), TIn, TRes>), dim3(p.groups), dim3(S::NT), 0,
+                                   st, p);
+        };
+        p.vec ? go(std::true_type()) : go(std::false_type());
     });
 }
 

@@ -10,8 +10,8 @@ namespace {
 
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
-    __shared__ float red[2][S::NT / 64][1];
-    RowSum<S, 1> sum{red};
+    __shared__ float red[2][S::NT / 64][2];
+    RowSum<S> sum{red};
     const int lane = threadIdx.x % S::TPR;
     const int sub = threadIdx.x / S::TPR;
     const float inv = 1.0f / static_cast<float>(p.D);
@@ -88,7 +88,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_fwd_kernel(NormParams p) {
         }
         const auto out = norm_rsrc(p.x_out, p.res_bf16, rows);
 #pragma unroll
-        for (int k = 0; k < S::K; ++k) store_piece<S, VEC, false>(out, p.res_bf16, lane, sub, k, p.D, xo[k]);
+        for (int k = 0; k < S::K; ++k) store_piece<S, VEC, true>(out, p.res_bf16, lane, sub, k, p.D, xo[k]);
         if (p.pre) {
             ss[0] = 0.0f;
 #pragma unroll
@@ -123,9 +123,11 @@ void launch(const NormParams& p, hipStream_t st) {
 
 int norm_groups(int R, int D, bool backward) {
     int rows = 1, nt = 256;
-    with_shape(D, [&](auto s) { rows = decltype(s)::ROWS, nt = decltype(s)::NT; });
+    auto take = [&](auto s) { rows = decltype(s)::ROWS, nt = decltype(s)::NT; };
+    with_shape(D, take);
     const int steps = static_cast<int>((static_cast<int64_t>(R) + rows - 1) / rows);
-    const int most = (backward ? 512 : 1024) * 256 / nt;
+    // workgroups per compute unit (256): see NormShape
+    const int most = 256 * (nt == 256 ? (backward ? 2 : 3) : nt == 512 && !backward ? 2 : 1);
     return steps < most ? steps : most;
 }
 

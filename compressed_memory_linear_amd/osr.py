@@ -609,8 +609,8 @@ def lattice_osr_scan_fwd(v, mu_logit, state_in=None, *, gamma_logit=None, length
     save = save or saved is not None
 
     def call(st):
-        yy = torch.empty(v.shape, dtype=y_dtype, device=dev) if y is None else y
-        so = torch.empty(sshape, dtype=torch.float32, device=dev) if state_out is None else state_out
+        yy = torch.empty_like(v, dtype=y_dtype) if y is None else y
+        so = v.new_empty(sshape, dtype=torch.float32) if state_out is None else state_out
         sv, sbytes = _workspace(saved, lattice_osr_scan_saved_bytes(desc), dev) if save else (None, 0)
         ws, wbytes = _scan_workspace(desc, workspace, dev)
         rc = lib.lattice_osr_scan_fwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
@@ -638,15 +638,15 @@ def lattice_osr_scan_bwd(v, mu_logit, dy, dstate_out=None, *, saved, gamma_logit
     _check_tensor("dy", dy, v.shape, None, dev)
     if dstate_out is not None:
         _check_tensor("dstate_out", dstate_out, sshape, torch.float32, dev)
-    want = [("dv", v.shape, grad_dtype), ("dmu_logit", v.shape, grad_dtype)]
+    want = [("dv", v, v.shape, grad_dtype), ("dmu_logit", v, v.shape, grad_dtype)]
     if gamma_logit is not None:
-        want.append(("dgamma_logit", v.shape, grad_dtype))
-    want.append(("dstate_in", sshape, torch.float32))
+        want.append(("dgamma_logit", v, v.shape, grad_dtype))
+    want.append(("dstate_in", dstate_out, sshape, torch.float32))
     _check_grads(grads, want, dev)
     _check_cuda(v)
 
     def call(st):
-        g = _grads(grads, want, dev)
+        g = _grads(grads, want, v)
         sv, sbytes = _workspace(saved, 0, dev)
         ws, wbytes = _scan_workspace(desc, workspace, dev)
         rc = lib.lattice_osr_scan_bwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
@@ -663,16 +663,18 @@ def lattice_osr_scan_bwd(v, mu_logit, dy, dstate_out=None, *, saved, gamma_logit
 def _check_grads(grads, want, dev):
     if grads is None:
         return
-    for name, shape, dtype in want:
+    for name, _, shape, dtype in want:
         if name not in grads:
             raise ValueError(f"grads lacks {name}")
         _check_tensor(name, grads[name], shape, dtype, dev)
 
 
-def _grads(grads, want, dev):
+def _grads(grads, want, lead):
+    """The caller's gradients, or new ones on lead's device, each like the tensor it belongs to."""
     if grads is not None:
-        return {name: grads[name] for name, _, _ in want}
-    return {name: torch.empty(shape, dtype=dtype, device=dev) for name, shape, dtype in want}
+        return {name: grads[name] for name, *_ in want}
+    return {name: lead.new_empty(shape, dtype=dtype) if like is None else torch.empty_like(like, dtype=dtype)
+            for name, like, shape, dtype in want}
 
 
 def lattice_osr_scan_step(v, mu_logit, state_in, *, gamma_logit=None, input_weight: int = SCAN_COMPLEMENT,
@@ -690,7 +692,7 @@ def lattice_osr_scan_step(v, mu_logit, state_in, *, gamma_logit=None, input_weig
     _check_cuda(v)
 
     def call(st):
-        yy = torch.empty(v.shape, dtype=y_dtype, device=dev) if y is None else y
+        yy = torch.empty_like(v, dtype=y_dtype) if y is None else y
         so = torch.empty_like(state_in) if state_out is None else state_out
         rc = lib.lattice_osr_scan_step(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit),
                                        _ptr(state_in), _ptr(so), _ptr(yy), st)
@@ -771,8 +773,8 @@ def lattice_osr_norm_fwd(y=None, x=None, *, gate=None, gate_kind: int = GATE_GEL
     _check_cuda(lead)
 
     def call(st):
-        xo = torch.empty(lead.shape, dtype=res_dtype, device=dev) if x_out is None and y is not None else x_out
-        zz = torch.empty(lead.shape, dtype=in_dtype, device=dev) if z is None and pre_norm else z
+        xo = torch.empty_like(lead, dtype=res_dtype) if x_out is None and y is not None else x_out
+        zz = torch.empty_like(lead, dtype=in_dtype) if z is None and pre_norm else z
         rc = lib.lattice_osr_norm_fwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
                                       _ptr(w_pre), _ptr(xo), _ptr(zz), st)
         if rc != OK:
@@ -798,14 +800,14 @@ def lattice_osr_norm_bwd(y=None, x=None, dx_out=None, dz=None, *, gate=None, gat
     for name, t, dt in (("dx_out", dx_out, res_dtype), ("dz", dz, in_dtype)):
         if t is not None:
             _check_tensor(name, t, lead.shape, dt, dev)
-    want = [(n, t.shape, dt) for n, t, dt in (("dy", y, grad_dtype), ("dgate", gate, grad_dtype), ("dx", x, res_dtype),
+    want = [(n, t, t.shape, dt) for n, t, dt in (("dy", y, grad_dtype), ("dgate", gate, grad_dtype), ("dx", x, res_dtype),
                                               ("dw_post", w_post, torch.float32), ("dscale", scale, torch.float32),
                                               ("dw_pre", w_pre, torch.float32)) if t is not None]
     _check_grads(grads, want, dev)
     _check_cuda(lead)
 
     def call(st):
-        g = _grads(grads, want, dev)
+        g = _grads(grads, want, lead)
         sums = w_post is not None or scale is not None or w_pre is not None
         ws, wbytes = _workspace(workspace, lattice_osr_norm_bwd_workspace_bytes(desc) if sums else 0, dev)
         rc = lib.lattice_osr_norm_bwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
