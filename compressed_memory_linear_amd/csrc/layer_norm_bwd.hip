@@ -10,6 +10,10 @@
 // rows are held by each thread for its columns while its workgroup walks over
 // its rows; the workgroups' sums go to the workspace and are added in a fixed
 // order by a second kernel (no atomics: reruns agree bit for bit).
+//
+// Bound by HBM: R32768 D2048 bf16 with every operand moves 1.07 GB in 204 us, 5.3 TB/s (the
+// device's own copy of 1 GiB: 5.4); 82 vector operations per value keep the vector units 40 %
+// busy.  Rows of 64 values are bound by those operations (R65536: 15 us for 34 MB, 9 of them).
 #include "layer_norm.h"
 
 namespace layer {
@@ -271,6 +275,9 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
 // The same for wide rows, on 1024 threads of 128 registers each: the weights lie in LDS, every
 // thread's own where it alone finds them (with two pieces a thread, where they do not
 // fit, they are read from the cache and no row is loaded ahead), and the gates are taken twice.
+// R8192 D8192 bf16: 302 us, 3.6 TB/s (the kernel above, spilling: 885 us; this one with the weights from
+// the cache: 430); R4096 D16384: 707 us (2016).  Bound by latency: one workgroup per compute
+// unit, three sums over 16 waves per row, nothing else to run meanwhile.
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p) {
     constexpr bool kAhead = S::K == 1;
@@ -408,27 +415,33 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
 }
 
 // out[c] = sum over the workgroups of part[g][which][c]: 32 columns and 32 rows of
-// threads to a workgroup, each adding every 32nd row in order.
+// threads to a workgroup, each adding every 32nd row in order, 16 loads at a time, then a
+// tree over the rows of threads.  (A row past the last reads zero.)
 __global__ __launch_bounds__(1024) void layer_norm_cols_kernel(NormParams p) {
-    __shared__ float s[32][33];
+    __shared__ float s[32][32];
     const int which = blockIdx.y;
     float* out = which == 0 ? p.dw_post : which == 1 ? p.dscale : p.dw_pre;
     if (!out) return;
     const int l = threadIdx.x & 31, r = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + l;
+    const uint32_t row = 3 * p.D * 4;  // bytes
+    const auto part = rows_rsrc(p.part, 0, p.groups * row);
     float a = 0.0f;
-    if (c < p.D) {
-#pragma unroll 16
-        for (int g = r; g < p.groups; g += 32) a += p.part[(static_cast<int64_t>(g) * 3 + which) * p.D + c];
+    for (int g0 = r; g0 < p.groups; g0 += 32 * 16) {
+        float v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] = load_row<float>(part, c < p.D ? (g0 + 32 * i) * row + (which * p.D + c) * 4 : kOut);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) a += v[i];
     }
     s[r][l] = a;
-    __syncthreads();
-    if (r == 0 && c < p.D) {
-        float t = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) t += s[i][l];
-        out[c] = t;
+    for (int n = 16; n > 0; n /= 2) {
+        __syncthreads();
+        if (r < n) s[r][l] += s[r + n][l];
     }
+    if (r == 0 && c < p.D) out[c] = s[0][l];
 }
 
 template <typename TIn, typename TRes>

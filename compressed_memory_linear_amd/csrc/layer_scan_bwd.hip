@@ -10,6 +10,11 @@
 // front, r -> A r + R, with the same A as the forward's map, so the tiles hand r on
 // as the forward's do h (layer_chain.h), from the last to the first; each recomputes its h_{t-1}
 // from the state the forward saved before it, and nothing else of the forward is kept.
+//
+// Bound by HBM and, with few chains, by the tiles' waits for one another (bf16, D2048): B8 T4096 with
+// the writing intensity 940 MB in 195 us, 4.8 TB/s; B1 T65536 without 1.34 GB in 273 us, 4.9 TB/s.
+// Runs of 16 tokens (126 registers with the intensity): 8 tokens 578 us for the latter's training
+// step, 16 428, 24 408, but 334, 306 and 336 for the former's.
 #include "layer_chain.h"
 #include "layer_device.h"
 #include "layer_launch.h"
