@@ -180,6 +180,35 @@ def test_unaligned_buffers(off):
         assert torch.isnan(flat[:off]).all() and torch.isnan(flat[off + v.numel():]).all()
 
 
+@pytest.mark.parametrize("which", ["w_post", "scale", "w_pre"])
+def test_unaligned_weights(which):
+    t, o, dx_out, dz = make(9, 256, BF, BF, seed=13)
+    want = osr.lattice_osr_norm_bwd(**t, **o, dx_out=dx_out, dz=dz)
+    t[which] = torch.cat([t[which][:1], t[which]])[1:]
+    assert t[which].data_ptr() % 16 == 4
+    run_all(t, o, dx_out, dz)
+    assert all(torch.isfinite(v).all() for v in want.values())
+
+
+def test_most_rows():
+    """2^31 - 1 rows of one value: the copy a call without norms makes reaches every one of them."""
+    R = 2 ** 31 - 1
+    y = torch.arange(256, device="cuda").to(BF).repeat(R // 256 + 1)[:R].view(R, 1)
+    x_out, z = osr.lattice_osr_norm_fwd(y, post_norm=False, pre_norm=False)
+    assert z is None
+    for a in range(0, R, 1 << 28):
+        assert torch.equal(x_out[a:a + (1 << 28)], y[a:a + (1 << 28)])
+    with pytest.raises(ValueError, match="rows"):
+        osr.lattice_osr_norm_fwd(torch.empty((R + 1, 1), dtype=BF, device="cuda"), post_norm=False, pre_norm=False)
+
+
+def test_empty_rows_are_refused():
+    for shape in ((0, 8), (4, 0)):
+        with pytest.raises(osr.OSRError) as e:
+            osr.lattice_osr_norm_fwd(torch.zeros(shape, dtype=BF, device="cuda"))
+        assert e.value.status == osr.ERR_SHAPE
+
+
 def test_leading_dimensions():
     t, o, dx_out, dz = make(24, 40, BF, BF, seed=14)
     want = osr.lattice_osr_norm_fwd(**t, **o)

@@ -367,3 +367,42 @@ def test_offsets_past_32_bits():
     for k in ("dv", "dmu_logit", "dstate_in"):
         assert torch.equal(g[k][-1], gw[k][0]), k
         assert (g[k][:-1] == 0).all()
+
+
+def test_widest_rows():
+    """The most channels a call takes: a tile's rows reach the largest offsets; any 64 of them equal a call of
+    their own."""
+    T, D = 270, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(90)
+    v = torch.randn((1, T, D), generator=g, device="cuda")
+    f = torch.randn((1, T, D), generator=g, device="cuda") + 2
+    y, st, sv = osr.lattice_osr_scan_fwd(v, f, save=True)
+    gr = osr.lattice_osr_scan_bwd(v, f, y, saved=sv)
+    for c in (0, 12345 * 64, D - 64):
+        part = [t[..., c:c + 64].contiguous() for t in (v, f, y)]
+        y2, st2, sv2 = osr.lattice_osr_scan_fwd(part[0], part[1], save=True)
+        g2 = osr.lattice_osr_scan_bwd(part[0], part[1], part[2], saved=sv2)
+        assert torch.equal(y[..., c:c + 64], y2) and torch.equal(st[..., c:c + 64], st2)
+        for k in ("dv", "dmu_logit", "dstate_in"):
+            assert torch.equal(gr[k][..., c:c + 64], g2[k]), k
+    with pytest.raises(osr.OSRError):
+        osr.lattice_osr_scan_fwd(*[torch.zeros((1, 1, D + 1), dtype=BF, device="cuda")] * 2)
+
+
+def test_empty_batch_is_refused():
+    for shape in ((0, 4, 8), (2, 0, 8), (2, 4, 0)):
+        t = torch.zeros(shape, dtype=BF, device="cuda")
+        with pytest.raises(osr.OSRError) as e:
+            osr.lattice_osr_scan_fwd(t, t)
+        assert e.value.status == osr.ERR_SHAPE
+
+
+def test_infinite_values_follow_the_formula():
+    """An infinite input makes its channel infinite until a gate of 0 meets it (0 times infinity: NaN), and no other."""
+    x = make(1, 600, 64, F, seed=91, gamma=False)
+    x["v"][0, 100, 3] = math.inf
+    x["mu_logit"][0, 400, 3] = -math.inf
+    y, _ = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], input_weight=osr.SCAN_ONE)
+    assert torch.isfinite(y[0, :100]).all() and torch.isinf(y[0, 100:400, 3]).all() and torch.isnan(y[0, 400:, 3]).all()
+    keep = torch.arange(64, device="cuda") != 3
+    assert torch.isfinite(y[..., keep]).all()
