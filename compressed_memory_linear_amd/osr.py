@@ -10,6 +10,7 @@ the first call raises; there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -160,6 +161,9 @@ def _check_tensor(name, t, shape, dtype, device=None):
     """Shape, dtype and layout of one argument, then its device: the kernels
     index every buffer by the descriptor's sizes, so a mismatch would read or
     write past it on the GPU."""
+    if (t.shape == shape and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+            and (device is None or t.device == device)):
+        return
     if tuple(t.shape) != tuple(shape):
         _shape_error(name, t, shape)
     if dtype is not None and t.dtype != dtype:
@@ -549,6 +553,19 @@ def make_scan_desc(B, T, D, in_dtype=BF16, y_dtype=F32, grad_dtype=F32, input_we
     return lattice_osr_scan_desc(B, T, D, in_dtype, y_dtype, grad_dtype, input_weight)
 
 
+@functools.lru_cache(maxsize=1024)
+def _scan_sizes(fields):
+    """(saved, workspace) bytes of a scan descriptor, given its fields."""
+    desc = lattice_osr_scan_desc(*fields)
+    return (_bytes_of("lattice_osr_scan_saved_bytes", desc), _bytes_of("lattice_osr_scan_workspace_bytes", desc))
+
+
+@functools.lru_cache(maxsize=1024)
+def _norm_size(fields):
+    """Workspace bytes of a norm descriptor's backward, given its fields."""
+    return _bytes_of("lattice_osr_norm_bwd_workspace_bytes", lattice_osr_norm_desc(*fields))
+
+
 def lattice_osr_scan_saved_bytes(desc: lattice_osr_scan_desc) -> int:
     return _bytes_of("lattice_osr_scan_saved_bytes", desc)
 
@@ -558,9 +575,9 @@ def lattice_osr_scan_workspace_bytes(desc: lattice_osr_scan_desc) -> int:
 
 
 def _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, grad_dtype, input_weight):
-    """Descriptor of a scan call, after checking every input against it: v,
+    """Descriptor fields of a scan call, after checking every input against them: v,
     mu_logit, gamma_logit [B,T,D] or [B,T,H,d] in one dtype, lengths [B] int32;
-    all contiguous, on one GPU.  Returns it with the states' shape."""
+    all contiguous, on one GPU.  Returns them with the states' shape."""
     if v.dim() not in (3, 4):
         raise ValueError("v/mu_logit/gamma_logit are [B,T,D] or [B,T,H,d]")
     if v.dtype not in _DT:
@@ -577,12 +594,15 @@ def _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, grad_dtype, input_wei
     D = shape[2] if len(shape) == 3 else shape[2] * shape[3]
     if max(shape[0], shape[1], D) > 2 ** 31 - 1:
         raise ValueError(f"shape {tuple(shape)}: sizes are at most 2^31 - 1")
-    desc = lattice_osr_scan_desc(shape[0], shape[1], D, _DT[v.dtype], _DT[y_dtype], _DT[grad_dtype], input_weight)
-    return desc, (shape[0], *shape[2:])
+    fields = (shape[0], shape[1], D, _DT[v.dtype], _DT[y_dtype], _DT[grad_dtype], input_weight)
+    return fields, (shape[0], *shape[2:])
 
 
-def _scan_workspace(desc, workspace, device):
-    return _workspace(workspace, lattice_osr_scan_workspace_bytes(desc), device)
+def _room(t, need, lead):
+    """(the caller's buffer or a new one of `need` bytes beside lead, its bytes); (None, 0) where neither is."""
+    if t is not None:
+        return _workspace(t, need, lead.device)
+    return (lead.new_empty(need, dtype=torch.uint8), need) if need else (None, 0)
 
 
 def lattice_osr_scan_fwd(v, mu_logit, state_in=None, *, gamma_logit=None, lengths=None,
@@ -598,7 +618,7 @@ def lattice_osr_scan_fwd(v, mu_logit, state_in=None, *, gamma_logit=None, length
     Returns (y, state_out) and, with save (or `saved`, a uint8 tensor of
     lattice_osr_scan_saved_bytes), what lattice_osr_scan_bwd needs."""
     lib = load_library()
-    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, torch.float32, input_weight)
+    fields, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, y_dtype, torch.float32, input_weight)
     dev = v.device
     for name, t in (("state_in", state_in), ("state_out", state_out)):
         if t is not None:
@@ -611,8 +631,10 @@ def lattice_osr_scan_fwd(v, mu_logit, state_in=None, *, gamma_logit=None, length
     def call(st):
         yy = torch.empty_like(v, dtype=y_dtype) if y is None else y
         so = v.new_empty(sshape, dtype=torch.float32) if state_out is None else state_out
-        sv, sbytes = _workspace(saved, lattice_osr_scan_saved_bytes(desc), dev) if save else (None, 0)
-        ws, wbytes = _scan_workspace(desc, workspace, dev)
+        snb, wnb = _scan_sizes(fields)
+        sv, sbytes = _room(saved, snb, v) if save else (None, 0)
+        ws, wbytes = _room(workspace, wnb, v)
+        desc = lattice_osr_scan_desc(*fields)
         rc = lib.lattice_osr_scan_fwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
                                       _ptr(state_in), _ptr(so), _ptr(yy), _ptr(sv), sbytes, _ptr(ws), wbytes, st)
         if rc != OK:
@@ -633,7 +655,7 @@ def lattice_osr_scan_bwd(v, mu_logit, dy, dstate_out=None, *, saved, gamma_logit
     lib = load_library()
     if saved is None:
         raise ValueError("saved: the tensor lattice_osr_scan_fwd returned with save=True")
-    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, dy.dtype, grad_dtype, input_weight)
+    fields, sshape = _scan_desc(v, mu_logit, gamma_logit, lengths, dy.dtype, grad_dtype, input_weight)
     dev = v.device
     _check_tensor("dy", dy, v.shape, None, dev)
     if dstate_out is not None:
@@ -648,7 +670,8 @@ def lattice_osr_scan_bwd(v, mu_logit, dy, dstate_out=None, *, saved, gamma_logit
     def call(st):
         g = _grads(grads, want, v)
         sv, sbytes = _workspace(saved, 0, dev)
-        ws, wbytes = _scan_workspace(desc, workspace, dev)
+        ws, wbytes = _room(workspace, _scan_sizes(fields)[1], v)
+        desc = lattice_osr_scan_desc(*fields)
         rc = lib.lattice_osr_scan_bwd(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(lengths),
                                       _ptr(sv), sbytes, _ptr(dy), _ptr(dstate_out), _ptr(g["dv"]),
                                       _ptr(g["dmu_logit"]), _ptr(g.get("dgamma_logit")), _ptr(g["dstate_in"]),
@@ -682,7 +705,7 @@ def lattice_osr_scan_step(v, mu_logit, state_in, *, gamma_logit=None, input_weig
     """One token of lattice_osr_scan_fwd (T = 1) for every sequence; state_out
     may be state_in (in place).  Returns (y, state_out)."""
     lib = load_library()
-    desc, sshape = _scan_desc(v, mu_logit, gamma_logit, None, y_dtype, torch.float32, input_weight)
+    fields, sshape = _scan_desc(v, mu_logit, gamma_logit, None, y_dtype, torch.float32, input_weight)
     dev = v.device
     _check_tensor("state_in", state_in, sshape, torch.float32, dev)
     if state_out is not None:
@@ -694,8 +717,9 @@ def lattice_osr_scan_step(v, mu_logit, state_in, *, gamma_logit=None, input_weig
     def call(st):
         yy = torch.empty_like(v, dtype=y_dtype) if y is None else y
         so = torch.empty_like(state_in) if state_out is None else state_out
-        rc = lib.lattice_osr_scan_step(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit),
-                                       _ptr(state_in), _ptr(so), _ptr(yy), st)
+        desc = lattice_osr_scan_desc(*fields)
+        rc = lib.lattice_osr_scan_step(ctypes.byref(desc), _ptr(v), _ptr(mu_logit), _ptr(gamma_logit), _ptr(state_in),
+                                       _ptr(so), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_scan_step")
         return yy, so
@@ -714,7 +738,7 @@ def lattice_osr_norm_bwd_workspace_bytes(desc: lattice_osr_norm_desc) -> int:
 
 
 def _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre, eps, z_dtype, x_dtype, grad_dtype):
-    """Descriptor of a norm call, after checking every input against it: rows
+    """Descriptor fields of a norm call, after checking every input against them: rows
     [..., D] of y, gate (one dtype) and x, weights [D] float32; all contiguous,
     on one GPU."""
     lead = y if y is not None else x
@@ -742,9 +766,9 @@ def _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
     R = lead.numel() // D if D else 0
     if R > 2 ** 31 - 1:
         raise ValueError(f"{R} rows: at most 2^31 - 1")
-    desc = lattice_osr_norm_desc(R, D, _DT[in_dtype], _DT[res_dtype], _DT[grad_dtype],
-                                 gate_kind, int(post_norm and y is not None), int(pre_norm), eps)
-    return desc, lead, in_dtype, res_dtype
+    fields = (R, D, _DT[in_dtype], _DT[res_dtype], _DT[grad_dtype], gate_kind, int(post_norm and y is not None),
+              int(pre_norm), eps)
+    return fields, lead, in_dtype, res_dtype
 
 
 def lattice_osr_norm_fwd(y=None, x=None, *, gate=None, gate_kind: int = GATE_GELU, post_norm: bool = True,
@@ -759,7 +783,7 @@ def lattice_osr_norm_fwd(y=None, x=None, *, gate=None, gate_kind: int = GATE_GEL
     only z = x / rms(x) w_pre, in z_dtype (x's dtype if None).  x_out may be x (in place).
     Returns (x_out, z); x_out is None without y, z without pre_norm."""
     lib = load_library()
-    desc, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
+    fields, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
                                                  eps, z_dtype, x_dtype, torch.float32)
     dev = lead.device
     if z_dtype is not None and z_dtype != in_dtype:
@@ -775,6 +799,7 @@ def lattice_osr_norm_fwd(y=None, x=None, *, gate=None, gate_kind: int = GATE_GEL
     def call(st):
         xo = torch.empty_like(lead, dtype=res_dtype) if x_out is None and y is not None else x_out
         zz = torch.empty_like(lead, dtype=in_dtype) if z is None and pre_norm else z
+        desc = lattice_osr_norm_desc(*fields)
         rc = lib.lattice_osr_norm_fwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
                                       _ptr(w_pre), _ptr(xo), _ptr(zz), st)
         if rc != OK:
@@ -793,23 +818,25 @@ def lattice_osr_norm_bwd(y=None, x=None, dx_out=None, dz=None, *, gate=None, gat
     Returns a dict of dy, dgate (grad_dtype), dx (x's dtype) and dw_post, dscale, dw_pre (float32), each
     where its operand was passed, allocated unless passed in `grads` (dx may be dx_out)."""
     lib = load_library()
-    desc, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
+    fields, lead, in_dtype, res_dtype = _norm_desc(y, x, gate, gate_kind, post_norm, w_post, scale, pre_norm, w_pre,
                                                  eps, dz.dtype if dz is not None else None,
                                                  dx_out.dtype if dx_out is not None else None, grad_dtype)
     dev = lead.device
     for name, t, dt in (("dx_out", dx_out, res_dtype), ("dz", dz, in_dtype)):
         if t is not None:
             _check_tensor(name, t, lead.shape, dt, dev)
-    want = [(n, t, t.shape, dt) for n, t, dt in (("dy", y, grad_dtype), ("dgate", gate, grad_dtype), ("dx", x, res_dtype),
-                                              ("dw_post", w_post, torch.float32), ("dscale", scale, torch.float32),
-                                              ("dw_pre", w_pre, torch.float32)) if t is not None]
+    f32 = torch.float32
+    want = [(n, t, t.shape, dt) for n, t, dt in (("dy", y, grad_dtype), ("dgate", gate, grad_dtype),
+                                                 ("dx", x, res_dtype), ("dw_post", w_post, f32),
+                                                 ("dscale", scale, f32), ("dw_pre", w_pre, f32)) if t is not None]
     _check_grads(grads, want, dev)
     _check_cuda(lead)
 
     def call(st):
         g = _grads(grads, want, lead)
         sums = w_post is not None or scale is not None or w_pre is not None
-        ws, wbytes = _workspace(workspace, lattice_osr_norm_bwd_workspace_bytes(desc) if sums else 0, dev)
+        ws, wbytes = _room(workspace, _norm_size(fields) if sums else 0, lead)
+        desc = lattice_osr_norm_desc(*fields)
         rc = lib.lattice_osr_norm_bwd(ctypes.byref(desc), _ptr(y), _ptr(gate), _ptr(x), _ptr(w_post), _ptr(scale),
                                       _ptr(w_pre), _ptr(dx_out), _ptr(dz), _ptr(g.get("dy")), _ptr(g.get("dgate")),
                                       _ptr(g.get("dx")), _ptr(g.get("dw_post")), _ptr(g.get("dscale")),
