@@ -274,22 +274,21 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
 
 // The same for wide rows, on 1024 threads of 128 registers each.  What does not fit them lies in
 // LDS, where every thread finds its own and no other's: the weights with one piece a thread,
-// two of the three column sums with two (the weights are then read from the cache, and
-// no row is loaded ahead).  The gates are taken twice.
-// R8192 D8192 bf16: 302 us, 3.6 TB/s (the kernel above, spilling: 885 us; this one with the weights from
-// the cache: 430); R4096 D16384: 479 us, 2.2 TB/s (2016; with every sum in registers 707).  Bound by
-// latency: one workgroup per compute unit, three sums over 16 waves per row, nothing else
-// to run meanwhile.
+// two of the three column sums with two (the weights are then read from the cache).  No row is
+// loaded ahead, and the gates are taken twice.
+// R8192 D8192: bf16 252 us, 4.3 TB/s, fp32 467 us (the kernel above, spilling: 885 and 1946; this one
+// with the next row in flight, spilling: 298 and 737; with the weights from the cache too, 430
+// in bf16).  R4096 D16384 bf16: 479 us, 2.2 TB/s (2016; with every sum in registers 707).  Bound by latency: one
+// workgroup per compute unit, three sums over 16 waves per row, nothing else to run meanwhile.
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p) {
-    constexpr bool kAhead = S::K == 1;
+    constexpr bool kWeights = S::K == 1;  // in LDS
     __shared__ float red[2][S::NT / 64][2];
-    __shared__ float4 mine[kAhead ? 3 : 2][2 * S::K][S::NT];  // the weights, or the sums of dscale and dw_post
+    __shared__ float4 mine[kWeights ? 3 : 2][2 * S::K][S::NT];  // the weights, or the sums of dscale and dw_post
     RowSum<S> sum{red};
     const int lane = threadIdx.x;
     const float inv = 1.0f / static_cast<float>(p.D);
     float gpost[S::K][kE] = {}, gsc[S::K][kE] = {}, gpre[S::K][kE] = {};  // with two pieces gpre alone
-    Raw<TIn, TRes> next[S::K];
     auto get = [&](int n, int k, float (&o)[kE]) {
         const int t = anew(lane);
         const float4 a = mine[n][2 * k][t], b = mine[n][2 * k + 1][t];
@@ -299,8 +298,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
         mine[n][2 * k][lane] = make_float4(v[0], v[1], v[2], v[3]);
         mine[n][2 * k + 1][lane] = make_float4(v[4], v[5], v[6], v[7]);
     };
-    if (kAhead) {
-        fetch<S, VEC>(p, blockIdx.x, lane, 0, next);
+    if (kWeights) {
         for (int n = 0; n < 3; ++n) {
             float v[kE];
             load_weights<S, VEC>(n == 0 ? p.w_post : n == 1 ? p.scale : p.w_pre, lane, 0, p.D, v);
@@ -312,7 +310,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
         for (int k = 0; k < S::K; ++k) put(0, k, zero), put(1, k, zero);
     }
     auto weights = [&](int n, const float* from, int k, float (&o)[kE]) {
-        if constexpr (kAhead) {
+        if constexpr (kWeights) {
             get(n, 0, o);
         } else {
             load_weights<S, VEC>(from, anew(lane), k, p.D, o);
@@ -321,10 +319,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
     for (uint32_t it = blockIdx.x; it < static_cast<uint32_t>(p.R); it += gridDim.x) {
         const Rows rows = rows_of<S>(it, p.R, p.D);
         Raw<TIn, TRes> raw[S::K];
-        if (!kAhead) fetch<S, VEC>(p, it, lane, 0, next);
-#pragma unroll
-        for (int k = 0; k < S::K; ++k) raw[k] = next[k];
-        if (kAhead) fetch<S, VEC>(p, it + gridDim.x, lane, 0, next);
+        fetch<S, VEC>(p, it, lane, 0, raw);
         float u[S::K][kE], d[S::K][kE];
         float ss[1] = {0.0f};
 #pragma unroll
@@ -388,18 +383,18 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
             weights(0, p.w_post, k, wp);
             weights(1, p.scale, k, sc);
             float as[kE], ap[kE];  // the sums of dscale and dw_post
-            if constexpr (!kAhead) get(0, k, as), get(1, k, ap);
+            if constexpr (!kWeights) get(0, k, as), get(1, k, ap);
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
                 u[k][e] *= r1;  // n1
-                float &to_s = kAhead ? gsc[k][e] : as[e], &to_p = kAhead ? gpost[k][e] : ap[e];
+                float &to_s = kWeights ? gsc[k][e] : as[e], &to_p = kWeights ? gpost[k][e] : ap[e];
                 to_s = fmaf(d[k][e], u[k][e] * wp[e], to_s);
                 d[k][e] *= sc[e];
                 to_p = fmaf(d[k][e], u[k][e], to_p);
                 d[k][e] *= wp[e];
                 ss[0] = fmaf(d[k][e], u[k][e], ss[0]);
             }
-            if constexpr (!kAhead) put(0, k, as), put(1, k, ap);
+            if constexpr (!kWeights) put(0, k, as), put(1, k, ap);
         }
         if (p.post) {
             sum(ss);
@@ -424,7 +419,7 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p
             store_piece<S, VEC, true>(dgr, p.grad_bf16, lane, 0, k, p.D, o);
         }
     }
-    if constexpr (!kAhead) {
+    if constexpr (!kWeights) {
 #pragma unroll
         for (int k = 0; k < S::K; ++k) get(0, k, gsc[k]), get(1, k, gpost[k]);
     }
