@@ -43,8 +43,6 @@ __device__ __forceinline__ void fetch(const NormParams& p, uint32_t it, int lane
 // phi and phi' of a piece's gates.
 template <typename TIn>
 __device__ __forceinline__ void gates(int kind, const Piece<TIn>& raw, float (&phi)[kE], float (&dphi)[kE]) {
-#pragma unroll
-    for (int e = 0; e < kE; ++e) phi[e] = 1.0f, dphi[e] = 0.0f;
     if (kind == 1) {
 #pragma unroll
         for (int e = 0; e < kE; ++e) {
@@ -63,6 +61,9 @@ __device__ __forceinline__ void gates(int kind, const Piece<TIn>& raw, float (&p
             phi[e] = g * s;
             dphi[e] = s * fmaf(g, r, 1.0f);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kE; ++e) phi[e] = 1.0f, dphi[e] = 0.0f;
     }
 }
 // This workgroup's column sums g, into its row of the workspace.
@@ -93,34 +94,16 @@ __device__ __forceinline__ void put_columns(float* to, float* cols, int lane, in
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     __shared__ float red[2][S::NT / 64][2];
-    // column sums of the workgroup's row slots (S::ROWS > 1 only)
+    // column sums of the workgroup's row slots (where it has several)
     __shared__ float cols[S::ROWS > 1 ? S::ROWS : 1][S::ROWS > 1 ? S::TPR * kE : 1];
     RowSum<S> sum{red};
     const int lane = threadIdx.x % S::TPR;
     const int sub = threadIdx.x / S::TPR;
     const float inv = 1.0f / static_cast<float>(p.D);
 
-    struct Raw {
-        Piece<TIn> y, g, z;
-        Piece<TRes> x, d;
-    };
-    auto fetch = [&](uint32_t it, Raw (&o)[S::K]) {
-        const Rows rows = rows_of<S>(it, p.R, p.D);
-        const auto yr = norm_rsrc(p.y, sizeof(TIn) == 2, rows), gr = norm_rsrc(p.gate, sizeof(TIn) == 2, rows);
-        const auto zr = norm_rsrc(p.dz, sizeof(TIn) == 2, rows), xr = norm_rsrc(p.x, sizeof(TRes) == 2, rows);
-        const auto dr = norm_rsrc(p.dx_out, sizeof(TRes) == 2, rows);
-#pragma unroll
-        for (int k = 0; k < S::K; ++k) {
-            load_piece<S, VEC>(yr, lane, sub, k, p.D, o[k].y);
-            load_piece<S, VEC>(gr, lane, sub, k, p.D, o[k].g);
-            load_piece<S, VEC>(xr, lane, sub, k, p.D, o[k].x);
-            load_piece<S, VEC>(zr, lane, sub, k, p.D, o[k].z);
-            load_piece<S, VEC>(dr, lane, sub, k, p.D, o[k].d);
-        }
-    };
     const uint32_t steps = (static_cast<uint32_t>(p.R) + S::ROWS - 1) / S::ROWS;
-    Raw next[S::K];
-    fetch(blockIdx.x, next);
+    Raw<TIn, TRes> next[S::K];
+    fetch<S, VEC>(p, blockIdx.x, lane, sub, next);
     float wpost[S::K][kE], sc[S::K][kE], wpre[S::K][kE];
     float gpost[S::K][kE], gsc[S::K][kE], gpre[S::K][kE];
 #pragma unroll
@@ -138,41 +121,26 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
         float ss[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < S::K; ++k) {
-            const Raw raw = next[k];
+            const Raw<TIn, TRes> raw = next[k];
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
                 yv[k][e] = widen(raw.y.e[e]);
                 xo[k][e] = widen(raw.x.e[e]);
                 d[k][e] = widen(raw.d.e[e]);
                 t[k][e] = widen(raw.z.e[e]);
-                phi[k][e] = 1.0f, dphi[k][e] = 0.0f;
             }
-            if (p.gate_kind == 1) {
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const float g = widen(raw.g.e[e]);
-                    float cdf, ex;
-                    gelu_parts(g, cdf, ex);
-                    phi[k][e] = g * cdf;
-                    dphi[k][e] = fmaf(g * 0.39894228040143268f, ex, cdf);
-                }
-            } else if (p.gate_kind == 2) {
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const float g = widen(raw.g.e[e]);
-                    float s, r;
-                    sigmoid2<kAccurate<TIn>>(g, s, r);
-                    phi[k][e] = g * s;
-                    dphi[k][e] = s * fmaf(g, r, 1.0f);
-                }
-            }
+            gates(p.gate_kind, raw.g, phi[k], dphi[k]);
 #pragma unroll
             for (int e = 0; e < kE; ++e) {
                 const float u = yv[k][e] * phi[k][e];
                 ss[0] = fmaf(u, u, ss[0]);
             }
         }
-        fetch(it + gridDim.x, next);  // in flight while this row is worked on
+        // the next row, in flight while this one is worked on; kept in this place (the compiler moves it behind
+        // part of what follows, which costs 10 of 205 us)
+        __builtin_amdgcn_sched_barrier(0);
+        fetch<S, VEC>(p, it + gridDim.x, lane, sub, next);
+        __builtin_amdgcn_sched_barrier(0);
         float r1 = 1.0f;
         if (p.y) {
             if (p.post) {
@@ -244,32 +212,10 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
             }
         }
     }
-    // this workgroup's column sums
-    auto put = [&](float* to, float (&g)[S::K][kE]) {
-        if (S::ROWS == 1) {
-#pragma unroll
-            for (int k = 0; k < S::K; ++k)
-#pragma unroll
-                for (int e = 0; e < kE; ++e) {
-                    const int c = col_of<S, VEC>(lane, k, e);
-                    if (c < p.D) to[c] = g[k][e];
-                }
-        } else {
-            __syncthreads();
-#pragma unroll
-            for (int e = 0; e < kE; ++e) cols[sub][col_of<S, VEC>(lane, 0, e)] = g[0][e];
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.D; c += S::NT) {
-                float s = 0.0f;
-                for (int i = 0; i < S::ROWS; ++i) s += cols[i][c];
-                to[c] = s;
-            }
-        }
-    };
     float* part = p.part + static_cast<int64_t>(blockIdx.x) * 3 * p.D;
-    if (p.dw_post) put(part, gpost);
-    if (p.dscale) put(part + p.D, gsc);
-    if (p.dw_pre) put(part + 2 * p.D, gpre);
+    if (p.dw_post) put_columns<S, VEC>(part, &cols[0][0], lane, sub, p.D, gpost);
+    if (p.dscale) put_columns<S, VEC>(part + p.D, &cols[0][0], lane, sub, p.D, gsc);
+    if (p.dw_pre) put_columns<S, VEC>(part + 2 * p.D, &cols[0][0], lane, sub, p.D, gpre);
 }
 
 // The same for wide rows, on 1024 threads of 128 registers each.  What does not fit them lies in
