@@ -106,13 +106,15 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_fwd_kernel(Scan
     if (p.ws) from.begin();
     __syncthreads();
     const bool last = tile == active - 1;
+    const int waves = blockDim.x >> 6;
     if (wave == 0) {
         // the tile's map
 #pragma unroll
-        for (int w = 1; w < kScanWaves; ++w) {
-            H = fmaf(s.A[w][l], H, s.H[w][l]);
-            A *= s.A[w][l];
-        }
+        for (int w = 1; w < kScanWaves; ++w)
+            if (w < waves) {
+                H = fmaf(s.A[w][l], H, s.H[w][l]);
+                A *= s.A[w][l];
+            }
     }
     if (p.ws) {
         from.finish(last, before, A, H);
@@ -167,7 +169,7 @@ void launch(bool step, const ScanParams& p, hipStream_t st) {
     if (!step) {
         const unsigned chains = static_cast<unsigned>(tiles_of(p.D, 64)) * p.B;
         hipLaunchKernelGGL((layer_scan_fwd_kernel<TIn, WT, GAMMA>), dim3(chains * tiles_of(p.T, kFwdTile)),
-                           dim3(kScanWaves * 64), 0, st, p);
+                           dim3(scan_threads(p.T, kFwdRun)), 0, st, p);
         return;
     }
     // four neighbours a thread where every buffer is aligned for it

@@ -115,14 +115,16 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_bwd_kernel(Scan
     Carry from{s, links, me.chain, rank, wave, l};
     if (p.ws) from.begin();
     __syncthreads();
+    const int waves = blockDim.x >> 6;
     if (wave == 0) {
         // the tile's map of r: the last run first
         A = 1.0f, R = 0.0f;
 #pragma unroll
-        for (int w = kScanWaves - 1; w >= 0; --w) {
-            R = fmaf(s.A[w][l], R, s.H[w][l]);
-            A *= s.A[w][l];
-        }
+        for (int w = kScanWaves - 1; w >= 0; --w)
+            if (w < waves) {
+                R = fmaf(s.A[w][l], R, s.H[w][l]);
+                A *= s.A[w][l];
+            }
     }
     const bool last = tile == 0;
     if (p.ws) {
@@ -134,7 +136,7 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_bwd_kernel(Scan
     float r = s.carry[l];
     if (p.dstate_in && last && wave == 0 && live) p.dstate_in[sc] = len > 0 ? fmaf(A, r, R) : r;
     for (int w = 0; w < wave; ++w) h = fmaf(s.A[w][l], h, sH[w][l]);
-    for (int w = kScanWaves - 1; w > wave; --w) r = fmaf(s.A[w][l], r, s.H[w][l]);
+    for (int w = waves - 1; w > wave; --w) r = fmaf(s.A[w][l], r, s.H[w][l]);
 
     // Second pass, forwards: what l_t is multiplied with.  om becomes the factor of df, wg is that of
     // dv and gam that of dg.
@@ -186,8 +188,8 @@ template <typename TIn, typename TDy>
 int pick(const ScanParams& p, hipStream_t st) {
     const unsigned groups = static_cast<unsigned>(tiles_of(p.D, 64) * p.B * tiles_of(p.T, kBwdTile));
     auto go = [&](auto wt, auto gamma) {
-        hipLaunchKernelGGL((layer_scan_bwd_kernel<TIn, TDy, wt(), gamma()>), dim3(groups), dim3(kScanWaves * 64), 0, st,
-                           p);
+        hipLaunchKernelGGL((layer_scan_bwd_kernel<TIn, TDy, wt(), gamma()>), dim3(groups),
+                           dim3(scan_threads(p.T, kBwdRun)), 0, st, p);
     };
     const std::integral_constant<int, 0> w0;
     const std::integral_constant<int, 1> w1;
