@@ -217,6 +217,16 @@ def test_leading_dimensions():
     assert got[0].shape == (2, 3, 4, 40) and torch.equal(got[0].view(24, 40), want[0])
 
 
+@pytest.mark.parametrize("D", [64, 2048, 5000, 10000])
+def test_workspace_contents_do_not_matter(D):
+    t, o, dx_out, dz = make(700, D, BF, BF, seed=18)
+    want = osr.lattice_osr_norm_bwd(**t, **o, dx_out=dx_out, dz=dz)
+    n = osr.lattice_osr_norm_bwd_workspace_bytes(osr.make_norm_desc(700, D, gate_kind=o["gate_kind"]))
+    ws = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")
+    g = osr.lattice_osr_norm_bwd(**t, **o, dx_out=dx_out, dz=dz, workspace=ws[:n])
+    assert all(torch.equal(g[k], want[k]) for k in want) and (ws[n:] == 255).all()
+
+
 def test_reruns_streams_and_graphs():
     t, o, dx_out, dz = make(3000, 256, BF, BF, seed=15)
 

@@ -193,6 +193,25 @@ def test_nan_stays_in_its_channel_and_behind():
     assert torch.equal(torch.isnan(st), bad[:, -1])
 
 
+def test_any_nan_passes_from_tile_to_tile():
+    """A NaN of any bits (all ones is what an empty hand-off word looks like) in a logit or a value reaches the end of
+    its channel, over every level of the hand-off, and no other channel."""
+    T = 17000
+    x = make(1, T, 64, F, seed=20, mean=3.0)
+    bits = x["mu_logit"].view(torch.int32)
+    bits[0, 10, 3], bits[0, 3000, 4], bits[0, 16000, 5] = -1, 0x7f800001, -1
+    x["v"].view(torch.int32)[0, 500, 6] = -1
+    y, st, sv = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], gamma_logit=x["gamma_logit"], save=True)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    for t, c in ((10, 3), (3000, 4), (16000, 5), (500, 6)):
+        bad[0, t:, c] = True
+    assert torch.equal(torch.isnan(y), bad)
+    g = osr.lattice_osr_scan_bwd(x["v"], x["mu_logit"], torch.ones_like(y), saved=sv, gamma_logit=x["gamma_logit"])
+    keep = [c for c in range(64) if c not in (3, 4, 5, 6)]
+    assert all(torch.isfinite(t[..., keep]).all() for t in g.values())
+    assert torch.isnan(g["dstate_in"][0, [3, 4, 5]]).all()
+
+
 @pytest.mark.parametrize("off", [1, 2, 3])
 def test_unaligned_buffers(off):
     """Views that start `off` elements into an allocation, every buffer of the call among them, and
@@ -291,6 +310,30 @@ def test_reruns_agree_bit_for_bit():
         got = [y, st, *g.values()]
         first = first or got
         assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_workspace_contents_do_not_matter():
+    """Whatever the workspace and `saved` hold on entry, hand-off words that look filled among it; nothing is
+    written behind either."""
+    B, T, D = 2, 20000, 130
+    x = make(B, T, D, BF, seed=47, mean=3.0)
+    dy, dso = grads_of(B, T, D, BF)
+    desc = osr.make_scan_desc(B, T, D, osr.BF16, osr.BF16, osr.F32)
+    wn, sn = osr.lattice_osr_scan_workspace_bytes(desc), osr.lattice_osr_scan_saved_bytes(desc)
+    first = None
+    for fill in (0, 255, 0x3f, 0x7f, None):
+        ws, sv = (torch.empty(n + 256, dtype=torch.uint8, device="cuda") for n in (wn, sn))
+        for t in (ws, sv):
+            t.random_(0, 256) if fill is None else t.fill_(fill)
+        tails = [ws[wn:].clone(), sv[sn:].clone()]
+        y, st, _ = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], gamma_logit=x["gamma_logit"],
+                                            y_dtype=BF, saved=sv[:sn], workspace=ws[:wn])
+        g = osr.lattice_osr_scan_bwd(x["v"], x["mu_logit"], dy, dso, saved=sv[:sn], gamma_logit=x["gamma_logit"],
+                                     workspace=ws[:wn])
+        got = [y, st, *g.values()]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got)), fill
+        assert torch.equal(ws[wn:], tails[0]) and torch.equal(sv[sn:], tails[1]), fill
 
 
 def test_two_streams_at_once():
