@@ -41,9 +41,10 @@ int check_scan(const lattice_osr_scan_desc* d) {
     if (d->B <= 0 || d->T <= 0 || d->D <= 0) return LATTICE_OSR_ERR_SHAPE;
     if (d->T > (1 << 30) || d->D > (1 << 20)) return LATTICE_OSR_ERR_SHAPE;
     if (static_cast<int64_t>(d->B) * d->T > (INT64_C(1) << 40) / d->D) return LATTICE_OSR_ERR_SHAPE;
-    // a launch has fewer than 2^32 threads: at most 1024 for each tile of 64 channels
+    // A launch has fewer than 2^32 threads: at most 1024 for each tile of 64 channels.  (The product
+    // is at most 65 x 129 / 2^13 times B T D, which the line before bounds.)
     const int64_t tiles = layer::tiles_of(d->T, layer::kBwdTile);
-    if ((static_cast<int64_t>(d->D) + 63) / 64 * d->B >= (INT64_C(1) << 22) / tiles) return LATTICE_OSR_ERR_SHAPE;
+    if (layer::tiles_of(d->D, 64) * d->B * tiles >= INT64_C(1) << 22) return LATTICE_OSR_ERR_SHAPE;
     if (!dtype_ok(d->in_dtype) || !dtype_ok(d->y_dtype) || !dtype_ok(d->grad_dtype)) return LATTICE_OSR_ERR_UNSUPPORTED;
     if (d->input_weight < LATTICE_OSR_SCAN_ONE || d->input_weight > LATTICE_OSR_SCAN_NORM)
         return LATTICE_OSR_ERR_UNSUPPORTED;

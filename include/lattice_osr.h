@@ -433,10 +433,10 @@ LATTICE_OSR_API int lattice_osr_glue_post(const lattice_osr_desc* desc, const vo
  *                             token (state_in where there is none).  Values
  *                             outside [0, T] are taken as the nearer end.
  * mu_logit = -inf drops the state before a token (a document's border inside a
- * row), +inf keeps it; either has a zero gradient.  D up to 2^20 and T up
- * to 2^30, odd ones included; element alignment only (rows move in wider pieces
- * where D and the addresses allow).  B ceil(D / 64) ceil(T / 128) must stay
- * below 2^22.
+ * row), +inf keeps it; either has a zero gradient.  D up to 2^20, odd ones
+ * included; element alignment only (rows move in wider pieces where D and the
+ * addresses allow).  B ceil(D / 64) ceil(T / 128) must stay below 2^22, which
+ * for one sequence of up to 64 channels means T up to 2^29 - 128.
  */
 #define LATTICE_OSR_SCAN_ONE 0        /* w = 1                  */
 #define LATTICE_OSR_SCAN_COMPLEMENT 1 /* w = 1 - mu             */

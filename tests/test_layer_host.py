@@ -292,3 +292,19 @@ def test_scan_workspace():
         assert call(d, p, ws=WS + 8) == osr.ERR_ALIGN
         for n in names:
             assert call(d, p, ws=p[n]) == osr.ERR_ALIAS, n
+
+
+@pytest.mark.parametrize("B,D,tiles", [(1, 64, (1 << 22) - 1), (1, 1, (1 << 21) + 1), (3, 64, 1398101), (1, 129, 1398101),
+                                       ((1 << 22) - 1, 64, 1), (5, 100, 419430)])
+def test_scan_size_limit(B, D, tiles):
+    """B ceil(D / 64) ceil(T / 128) below 2^22, that product itself: the largest T inside is taken, one token more
+    is refused where it begins the tile that reaches the limit."""
+    chains = B * ((D + 63) // 64)
+    assert chains * tiles < 1 << 22
+    T = tiles * 128
+    assert osr.lattice_osr_scan_saved_bytes(osr.make_scan_desc(B, T, D)) == B * tiles * D * 4
+    if chains * (tiles + 1) >= 1 << 22:
+        d = osr.make_scan_desc(B, T + 1, D)
+        with pytest.raises(osr.OSRError):
+            osr.lattice_osr_scan_saved_bytes(d)
+        assert _fwd(d, _fake(*FWD)) == osr.ERR_SHAPE

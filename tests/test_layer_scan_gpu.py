@@ -449,3 +449,24 @@ def test_infinite_values_follow_the_formula():
     assert torch.isfinite(y[0, :100]).all() and torch.isinf(y[0, 100:400, 3]).all() and torch.isnan(y[0, 400:, 3]).all()
     keep = torch.arange(64, device="cuda") != 3
     assert torch.isfinite(y[..., keep]).all()
+
+
+def test_longest_sequences():
+    """One channel past 2^28 tokens, more than half of the tiles that a call takes: what follows a dropped state
+    equals a call of its own, and so does the beginning."""
+    p, T = 1 << 28, (1 << 28) + 3 * 16384 + 777
+    g = torch.Generator(device="cuda").manual_seed(92)
+    v, f, dy = (torch.randn((1, T, 1), generator=g, device="cuda", dtype=BF) for _ in range(3))
+    f += 2
+    f[0, p] = -math.inf
+    y, st, sv = osr.lattice_osr_scan_fwd(v, f, y_dtype=BF, save=True)
+    gr = osr.lattice_osr_scan_bwd(v, f, dy, saved=sv, grad_dtype=BF)
+    assert all(torch.isfinite(t).all() for t in (y, *gr.values()))
+    head = [t[:, :16384].contiguous() for t in (v, f)]
+    assert torch.equal(y[:, :16384], osr.lattice_osr_scan_fwd(*head, y_dtype=BF)[0])
+    part = [t[:, p:].contiguous() for t in (v, f, dy)]
+    y2, st2, sv2 = osr.lattice_osr_scan_fwd(part[0], part[1], y_dtype=BF, save=True)
+    g2 = osr.lattice_osr_scan_bwd(*part, saved=sv2, grad_dtype=BF)
+    assert torch.equal(y[:, p:], y2) and torch.equal(st, st2)
+    for k in ("dv", "dmu_logit"):
+        assert torch.equal(gr[k][:, p:], g2[k]), k
