@@ -38,15 +38,17 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&x)[V
 }
 
 // e^x through the hardware's 2^x.  Rounded to one float, the product x log2(e) costs a
-// relative |x| 2^-24 of the result; ACC keeps its error as a second part (4 operations
-// more).  For bf16 logits, known to 2^-9 of their value, the first form serves.
+// relative 1.2 |x| 2^-24 of the result (log2(e) as a float is 0.2 of that); ACC keeps what the
+// product and the constant lose as a second part (5 operations more; without the constant's
+// the result is off by 20 units at |x| = 80).  For bf16 logits, known to 2^-9 of their
+// value, the first form serves.
 template <bool ACC>
 __device__ __forceinline__ float exp_of(float x) {
-    constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147181f;
+    constexpr float kLog2e = 1.44269504088896341f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.693147181f;
     const float hi = x * kLog2e;
     const float e = __builtin_amdgcn_exp2f(hi);
     if constexpr (!ACC) return e;
-    const float lo = fmaf(x, kLog2e, -hi);
+    const float lo = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -hi));
     // past the range of 2^x the low part is not wanted (it is NaN at infinite x)
     return fabsf(hi) < 128.0f ? fmaf(e, lo * kLn2, e) : e;
 }

@@ -24,13 +24,18 @@ TINY = 1e-35  # what flushing subnormal numbers may cost
 ONE, COMPLEMENT, NORM = 0, 1, 2
 NONE, GELU, SILU = 0, 1, 2
 
-# sigmoid(x): e = 2^(x log2 e) off by |x| u (the rounded product; the callers that keep it in two
-# parts do better) and 6 u, 1 + e and 1 / x 3 u more; e s one more.
-E_SIG = 10 * U
+# sigmoid(x) and 1 - sigmoid(x), relative: e = 2^(x log2 e) by the hardware (2 u) with the exponent's low part
+# multiplied in (1 u), 1 + e (1 u), 1 / x (2 u), e s (1 u): 7 u, and 1 for what is of second order.  bf16
+# logits go without the low part: |x| u more for the rounded product, and 0.23 |x| u for the rounded log2 e, which
+# 2 u cover at logits of up to 8.
+E_SIG = 8 * U
 
 
 def _e_sig(x):
-    return E_SIG + U * x.abs().clamp(max=100.0)
+    """x as stored: its type decides how the exponent is formed."""
+    if x.dtype != torch.bfloat16:
+        return torch.full_like(x, E_SIG, dtype=torch.float64)
+    return E_SIG + 2 * U + U * x.double().abs().clamp(max=100.0)
 
 
 # ----------------------------------------------------------------- scan --
@@ -60,8 +65,8 @@ def scan(v, f, g=None, state_in=None, lengths=None, weight=COMPLEMENT, dy=None, 
     ok = _valid(lengths, B, T, dev)
     v, mu, om, gam, ngam, w, pull = _gates(v, f, g, weight)
     z = torch.zeros((), dtype=torch.float64, device=dev)
-    es = torch.where(ok, _e_sig(f.double()), z)                               # of mu and 1 - mu
-    eg = torch.where(ok, _e_sig(g.double()), z) if g is not None else z + 0 * es  # of gamma
+    es = torch.where(ok, _e_sig(f), z)                                         # of mu and 1 - mu
+    eg = torch.where(ok, _e_sig(g), z) if g is not None else torch.zeros_like(es)  # of gamma
     ec = es + eg + 12 * U  # of w(mu) gamma v: both gates, a root (its own 2 u), its argument, three products
     a = torch.where(ok, mu, z + 1)
     b = torch.where(ok, w * gam * v, z)
@@ -118,12 +123,15 @@ def _act(kind, g):
     GeLU: erfc to a few units (2^-20), and in the lower tail the rounding of its argument
     moves Phi by a relative g^2 u twice over; SiLU: the sigmoid's error and a product."""
     if kind == GELU:
+        g = g.double()
         cdf = 0.5 * torch.erfc(-g * math.sqrt(0.5))
         pdf = torch.exp(-0.5 * g * g) / math.sqrt(2 * math.pi)
         rel = 2.0 ** -20 + 2 * g * g * U + 4 * U
         return g * cdf, cdf + g * pdf, rel, rel * cdf + (g * pdf).abs() * (16 * U + g * g * U) + 2 * U
+    es = _e_sig(g)
+    g = g.double()
     s, r = torch.sigmoid(g), torch.sigmoid(-g)
-    return g * s, s * (1 + g * r), _e_sig(g) + 2 * U, (3 * _e_sig(g) + 4 * U) * s * (1 + (g * r).abs())
+    return g * s, s * (1 + g * r), es + 2 * U, (3 * es + 4 * U) * s * (1 + (g * r).abs())
 
 
 def norm(y=None, x=None, gate=None, gate_kind=GELU, post=True, w_post=None, scale=None, pre=True, w_pre=None, eps=1e-6,
@@ -148,7 +156,7 @@ def norm(y=None, x=None, gate=None, gate_kind=GELU, post=True, w_post=None, scal
         yv = y.double()
         phi, dphi, ephi, edphi = one.expand(R, D), zero.expand(R, D), zero.expand(R, D), zero.expand(R, D)
         if gate is not None:
-            phi, dphi, ephi, edphi = _act(gate_kind, gate.double())
+            phi, dphi, ephi, edphi = _act(gate_kind, gate)
         u = yv * phi
         eu = u.abs() * (ephi + 2 * U)
         r1, er1 = one.expand(R, 1), zero.expand(R, 1)  # er1: relative

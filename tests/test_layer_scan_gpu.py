@@ -470,3 +470,25 @@ def test_longest_sequences():
     assert torch.equal(y[:, p:], y2) and torch.equal(st, st2)
     for k in ("dv", "dmu_logit"):
         assert torch.equal(gr[k][:, p:], g2[k]), k
+
+
+@pytest.mark.parametrize("call", ["step", "forward"])
+def test_gates_alone(call):
+    """mu, 1 - mu and gamma by themselves (y = mu 1 + 0, (1 - mu) 1 and gamma 1), logits from -80 to 80: fp32 within
+    8 units of 2^-24 of each gate's own value (2^x 2, its low part 1, 1 + e 1, 1 / x 2, e s 1, and 1 for what is of
+    second order); bf16 logits, whose exponent is one rounded product, within 8 and 1.25 |x| more."""
+    x = torch.cat([torch.linspace(-80, 80, 20001), torch.linspace(-3, 3, 3000)]).cuda().view(1, 1, -1)
+    for dtype in (F, BF):
+        f = x.to(dtype)
+        one, zero = torch.ones_like(f), torch.zeros_like(f)
+        st = torch.ones((1, f.shape[-1]), device="cuda")
+        run = osr.lattice_osr_scan_step if call == "step" else osr.lattice_osr_scan_fwd
+        mu, _ = run(zero, f, st)
+        om, _ = run(one, f, 0 * st)
+        gam, _ = run(one, zero, 0 * st, gamma_logit=f, input_weight=osr.SCAN_ONE)
+        lim = 8 * layer.U * (1 if dtype == F else 1 + 1.25 / 8 * f.double().abs())
+        for name, got, ref in (("mu", mu, torch.sigmoid(f.double())), ("1 - mu", om, torch.sigmoid(-f.double())),
+                               ("gamma", gam, torch.sigmoid(f.double()))):
+            worst = float(((got.double() / ref - 1).abs() / lim).max())
+            print(f"  {dtype} {name}: {worst:.3f}", flush=True)
+            assert worst <= 1, (dtype, name, worst)

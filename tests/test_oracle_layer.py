@@ -152,3 +152,34 @@ def test_norm_gradient_by_differences():
         h = 1e-5
         num = (loss(**{**k, n: k[n] + h * d}) - loss(**{**k, n: k[n] - h * d})) / (2 * h)
         assert num == pytest.approx(float((out["d" + n] * d).sum()), rel=1e-6, abs=1e-8), n
+
+
+def _gate_in_fp32(x, parts):
+    """sigmoid(x) and 1 - sigmoid(x) in fp32, every operation rounded: the exponent x log2(e) as one rounded product
+    (parts 0), with what the product loses (1), with what the rounded log2(e) loses too (2)."""
+    f32, f64 = torch.float32, torch.float64
+    r = lambda a: a.to(f32).to(f64)
+    x, c = -x.to(f64), r(torch.tensor(math.log2(math.e), dtype=f64))
+    hi = r(x * c)
+    e = r(torch.exp2(hi))
+    if parts:
+        lo = r(x * c - hi)
+        if parts == 2:
+            lo = r(x * r(math.log2(math.e) - c) + lo)
+        e = r(e * r(lo * r(torch.tensor(math.log(2.0), dtype=f64))) + e)
+    s = r(1 / r(1 + e))
+    return s, torch.where(e > 2.0 ** 25, torch.ones_like(e), r(e * s))
+
+
+def test_gate_bounds_tell_the_forms_of_the_exponent_apart():
+    """The bound for fp32 logits holds the form that keeps both low parts and neither of the others; the one for
+    bf16 logits holds the plain product."""
+    x = torch.linspace(-80, 80, 20001)
+    want = torch.sigmoid(x.double()), torch.sigmoid(-x.double())
+    worst = lambda x, parts: max(float(((a / b - 1).abs() / layer._e_sig(x)).max())
+                                 for a, b in zip(_gate_in_fp32(x, parts), want))
+    assert worst(x, 2) < 0.6
+    assert worst(x, 1) > 2 and worst(x, 0) > 6
+    x = torch.linspace(-8, 8, 257).bfloat16()
+    want = torch.sigmoid(x.double()), torch.sigmoid(-x.double())
+    assert worst(x, 0) <= 1
