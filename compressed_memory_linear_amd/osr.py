@@ -542,9 +542,15 @@ def _on(device, stream, fn):
             return fn(st.cuda_stream)
 
 
-def _bytes_of(fn, desc):
+def _query(fn, desc):
+    """What the library answers for a size; None for a descriptor that it refuses."""
     n = int(getattr(load_library(), fn)(ctypes.byref(desc)))
-    if n == ctypes.c_size_t(-1).value:
+    return None if n == ctypes.c_size_t(-1).value else n
+
+
+def _bytes_of(fn, desc):
+    n = _query(fn, desc)
+    if n is None:
         raise OSRError(ERR_SHAPE, fn)
     return n
 
@@ -555,15 +561,16 @@ def make_scan_desc(B, T, D, in_dtype=BF16, y_dtype=F32, grad_dtype=F32, input_we
 
 @functools.lru_cache(maxsize=1024)
 def _scan_sizes(fields):
-    """(saved, workspace) bytes of a scan descriptor, given its fields."""
+    """(saved, workspace) bytes of a scan descriptor, given its fields; zeros for one that the call
+    itself refuses, with its status."""
     desc = lattice_osr_scan_desc(*fields)
-    return (_bytes_of("lattice_osr_scan_saved_bytes", desc), _bytes_of("lattice_osr_scan_workspace_bytes", desc))
+    return (_query("lattice_osr_scan_saved_bytes", desc) or 0, _query("lattice_osr_scan_workspace_bytes", desc) or 0)
 
 
 @functools.lru_cache(maxsize=1024)
 def _norm_size(fields):
-    """Workspace bytes of a norm descriptor's backward, given its fields."""
-    return _bytes_of("lattice_osr_norm_bwd_workspace_bytes", lattice_osr_norm_desc(*fields))
+    """Workspace bytes of a norm descriptor's backward, given its fields; 0 as above."""
+    return _query("lattice_osr_norm_bwd_workspace_bytes", lattice_osr_norm_desc(*fields)) or 0
 
 
 def lattice_osr_scan_saved_bytes(desc: lattice_osr_scan_desc) -> int:

@@ -340,3 +340,18 @@ def test_layer_forward_and_backward():
         err = float((a.cpu().double() - b.detach()).abs().max() / b.detach().abs().max())
         print(f"  {n}: {err:.2e}", flush=True)
         assert err <= 1e-4, (n, err)
+
+
+def test_refusals_carry_the_library_s_status():
+    """Forward and backward refuse alike, also where the backward's workspace is asked for first."""
+    t, o, dx_out, dz = make(4, 64, BF, BF)
+    wide = torch.zeros((2, 16385), dtype=BF, device="cuda")
+    w = torch.ones(16385, device="cuda")
+    for call in (lambda: osr.lattice_osr_norm_fwd(**t, **{**o, "eps": 0.0}),
+                 lambda: osr.lattice_osr_norm_bwd(**t, **{**o, "eps": 0.0}, dx_out=dx_out, dz=dz),
+                 lambda: osr.lattice_osr_norm_bwd(**t, **{**o, "gate_kind": 7}, dx_out=dx_out, dz=dz),
+                 lambda: osr.lattice_osr_norm_fwd(wide, wide, w_post=w),
+                 lambda: osr.lattice_osr_norm_bwd(wide, wide, wide, wide, w_post=w)):
+        with pytest.raises(osr.OSRError) as e:
+            call()
+        assert e.value.status == osr.ERR_UNSUPPORTED

@@ -492,3 +492,16 @@ def test_gates_alone(call):
             worst = float(((got.double() / ref - 1).abs() / lim).max())
             print(f"  {dtype} {name}: {worst:.3f}", flush=True)
             assert worst <= 1, (dtype, name, worst)
+
+
+def test_refusals_carry_the_library_s_status():
+    """A descriptor that a call refuses is reported as the C ABI reports it, also where its sizes are asked first."""
+    x = make(2, 200, 40, BF)
+    y, _, saved = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], save=True)
+    for bad in (-1, 3):
+        for call in (lambda: osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], input_weight=bad),
+                     lambda: osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], input_weight=bad, save=True),
+                     lambda: osr.lattice_osr_scan_bwd(x["v"], x["mu_logit"], y, saved=saved, input_weight=bad)):
+            with pytest.raises(osr.OSRError) as e:
+                call()
+            assert e.value.status == osr.ERR_UNSUPPORTED
