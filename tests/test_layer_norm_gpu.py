@@ -355,3 +355,41 @@ def test_refusals_carry_the_library_s_status():
         with pytest.raises(osr.OSRError) as e:
             call()
         assert e.value.status == osr.ERR_UNSUPPORTED
+
+
+# Rows that give every workgroup of either direction (at most 768) several, none of them zeros: running column
+# sums, and row sums that follow one another through the same LDS.  Vector and element layouts of every width's kernel.
+MANY = [(20000, 64), (20000, 61), (9000, 200), (5000, 512), (5000, 777), (2000, 2048), (2000, 1025), (1300, 4096),
+        (1300, 2050), (700, 4104), (700, 5001), (700, 8192), (700, 8200), (700, 8191), (700, 12345), (700, 16384),
+        (700, 16383)]
+
+
+@pytest.mark.parametrize("R,D", MANY)
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_several_rows_per_workgroup(R, D, dtype):
+    for gate in ("gelu", "silu"):
+        run_all(*make(R, D, dtype, dtype, gate, seed=R + D), grad_dtype=dtype, res_dtype=dtype)
+
+
+@pytest.mark.parametrize("R,D", [(9000, 96), (2000, 2000), (1300, 4000), (600, 5000), (600, 5001), (600, 9000), (600, 9001)])
+@pytest.mark.parametrize("gate", ["gelu", "silu", None])
+@pytest.mark.parametrize("post", [True, False])
+def test_combinations_over_several_rows(R, D, gate, post):
+    for x in (True, False):
+        for pre in (True, False):
+            for scale in (True, False):
+                run_all(*make(R, D, F, F, gate, post, x, scale, pre, seed=23), res_dtype=F)
+
+
+@pytest.mark.parametrize("R,D", [(2000, 2000), (600, 5000), (600, 5001), (600, 9000), (600, 9001)])
+def test_types_and_absent_operands_over_several_rows(R, D):
+    for in_dtype, res_dtype, grad_dtype in ((BF, F, BF), (BF, F, F), (F, BF, F), (F, BF, BF), (BF, BF, F), (F, F, BF)):
+        run_all(*make(R, D, in_dtype, res_dtype, seed=24), grad_dtype=grad_dtype, res_dtype=res_dtype)
+    run_all(*make(R, D, BF, BF, y=False, seed=25))
+    run_all(*make(R, D, F, F, y=False, weights=False, seed=25), res_dtype=F)
+    run_all(*make(R, D, BF, F, weights=False, scale=False, seed=26), res_dtype=F)
+    t, o, _, dz = make(R, D, BF, BF, seed=27)
+    g = osr.lattice_osr_norm_bwd(**t, **o, dx_out=None, dz=dz)
+    out, bound = oracle(t, o, None, dz, True)
+    for n in g:
+        check(n, g[n], out[n], bound[n])
