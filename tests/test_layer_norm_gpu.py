@@ -393,3 +393,17 @@ def test_types_and_absent_operands_over_several_rows(R, D):
     out, bound = oracle(t, o, None, dz, True)
     for n in g:
         check(n, g[n], out[n], bound[n])
+
+
+@pytest.mark.parametrize("kind", [osr.GATE_GELU, osr.GATE_SILU])
+@pytest.mark.parametrize("dtype", [F, BF])
+def test_gates_alone(kind, dtype):
+    """phi and phi' by themselves (y, scale and the incoming gradient 1, neither norm), far into both tails."""
+    g = torch.cat([torch.linspace(-13, 13, 30000), torch.linspace(-2, 2, 2768)]).view(64, 512).to(dtype).cuda()
+    one = torch.ones_like(g)
+    phi, _ = osr.lattice_osr_norm_fwd(one, None, gate=g, gate_kind=kind, post_norm=False, pre_norm=False, x_dtype=F)
+    d = osr.lattice_osr_norm_bwd(one, None, one.float(), gate=g, gate_kind=kind, post_norm=False, pre_norm=False)
+    want, dwant, rel, dabs = layer._act(kind, g)
+    for name, got, ref, lim in (("phi", phi, want, rel * want.abs()), ("phi'", d["dgate"], dwant, dabs),
+                                ("dy", d["dy"], want, rel * want.abs())):
+        check(name, got, ref, lim + layer.TINY)
