@@ -47,6 +47,28 @@ struct Chain {
     }
 };
 
+// The product of two runs' A, each in [0, 1].  Where it underflows although neither is 0 it is the
+// least positive number: an infinite state before it stays infinite, as token by token, and does
+// not become 0 inf.  (Beside a finite state the two differ by 2^-149 of it.)  A NaN may
+// be lost here; the run's H or R is NaN with it.  Three operations: the same with comparisons
+// and a selection, in the chain's own latency, cost the training step of B1 T65536 D2048 444 -> 451 us.
+constexpr float kLeast = 1.40129846e-45f;
+__device__ __forceinline__ float times(float a, float b) {
+    return fmaxf(a * b, fminf(fminf(a, b), kLeast));
+}
+// The same for a run's product A over its gates: told from a gate of 0 where it is 0 (a branch that
+// only waves with such a product take).
+template <int N>
+__device__ __forceinline__ float run_product(float A, const float (&a)[N]) {
+    if (__any(A == 0.0f)) {
+        float least = a[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) least = fminf(least, a[i]);
+        if (A == 0.0f && least > 0.0f) A = kLeast;
+    }
+    return A;
+}
+
 __device__ __forceinline__ void put_pair(uint64_t* p, float a, float b) {
     // a NaN could look empty; any other NaN says the same
     const uint32_t x = a != a ? 0x7fc00000u : __float_as_uint(a);
@@ -110,7 +132,7 @@ struct Carry {
         a = 1.0f, h = 0.0f;
         for (int k = 1; k <= n; ++k) {
             h = fmaf(A[k][l], h, H[k][l]);
-            a *= A[k][l];
+            a = times(a, A[k][l]);
         }
     }
     // After that barrier; wave 0 holds the tile's own map (A, H) and the state before the chain, `first`.
@@ -132,7 +154,7 @@ struct Carry {
             __syncthreads();
             if (wave == 0) {
                 compose(W - 1, s.PA, s.PH, a, h);
-                a *= A;
+                a = times(a, A);
                 asm volatile("" : "+v"(a), "+v"(first));
                 put_pair(group_map(group()), a, fmaf(A, h, H));
             }

@@ -100,6 +100,7 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_fwd_kernel(Scan
             H = fmaf(a[i], H, x[i]);
         }
     }
+    A = run_product(A, a);
     s.A[wave][l] = A, s.H[wave][l] = H;
     const Chain links = chain_of(p.ws, chains, tiles);
     Carry from{s, links, me.chain, tile, wave, l};
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_fwd_kernel(Scan
         for (int w = 1; w < kScanWaves; ++w)
             if (w < waves) {
                 H = fmaf(s.A[w][l], H, s.H[w][l]);
-                A *= s.A[w][l];
+                A = times(A, s.A[w][l]);
             }
     }
     if (p.ws) {

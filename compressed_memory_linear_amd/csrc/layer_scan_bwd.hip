@@ -110,6 +110,7 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_bwd_kernel(Scan
     }
 #pragma unroll
     for (int i = kBwdRun - 1; i >= 0; --i) R = a[i] * (R + widen(ry[i]));
+    A = run_product(A, a);
     s.A[wave][l] = A, s.H[wave][l] = R, sH[wave][l] = H;
     const Chain links = chain_of(p.ws, chains, tiles);
     Carry from{s, links, me.chain, rank, wave, l};
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(kScanWaves * 64, 4) void layer_scan_bwd_kernel(Scan
         for (int w = kScanWaves - 1; w >= 0; --w)
             if (w < waves) {
                 R = fmaf(s.A[w][l], R, s.H[w][l]);
-                A *= s.A[w][l];
+                A = times(A, s.A[w][l]);
             }
     }
     const bool last = tile == 0;

@@ -505,3 +505,37 @@ def test_refusals_carry_the_library_s_status():
             with pytest.raises(osr.OSRError) as e:
                 call()
             assert e.value.status == osr.ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("T", [33, 300, 3000, 20000])
+@pytest.mark.parametrize("dtype", [F, BF])
+def test_infinite_states_stay_infinite_under_strong_forgetting(T, dtype):
+    """Gates whose product over a run underflows, none of them 0: an infinite state, input or incoming gradient is
+    infinite from there on, as token by token, at every level of the split; a gate of 0 still drops a finite one."""
+    x = make(1, T, 64, dtype, seed=93, mean=-4.0)
+    x["state_in"][0, 3], x["state_in"][0, 5] = math.inf, -math.inf
+    x["v"][0, T // 3, 7] = math.inf
+    x["mu_logit"][0, T // 2, 9] = -math.inf
+    for w in WEIGHTS:
+        y, st, sv = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], gamma_logit=x["gamma_logit"],
+                                             input_weight=w, save=True)
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        bad[0, :, [3, 5]] = True
+        bad[0, T // 3:, 7] = True
+        assert torch.equal(torch.isinf(y), bad) and not torch.isnan(y).any()
+        assert torch.equal(torch.isinf(st), bad[:, -1])
+        assert (y[0, :, 3] > 0).all() and (y[0, :, 5] < 0).all()
+        clean = {k: torch.nan_to_num(t, 0.0, 0.0, 0.0) if k in ("v", "state_in") else t for k, t in x.items()}
+        _, _, sv = osr.lattice_osr_scan_fwd(clean["v"], x["mu_logit"], clean["state_in"],
+                                            gamma_logit=x["gamma_logit"], input_weight=w, save=True)
+        dy, dso = grads_of(1, T, 64, F)
+        dso[0, 3], dso[0, 5] = math.inf, -math.inf
+        dy[0, T // 3, 7] = math.inf
+        g = osr.lattice_osr_scan_bwd(clean["v"], x["mu_logit"], dy, dso, saved=sv, gamma_logit=x["gamma_logit"],
+                                     input_weight=w)
+        bad = torch.zeros_like(y, dtype=torch.bool)
+        bad[0, :, [3, 5]] = True
+        bad[0, :T // 3 + 1, 7] = True
+        assert torch.equal(torch.isinf(g["dv"]), bad) and not torch.isnan(g["dv"]).any()
+        assert torch.equal(torch.isinf(g["dstate_in"]), bad[:, 0])
+        assert (g["dv"][0, :, 3] > 0).all() and (g["dv"][0, :, 5] < 0).all()
