@@ -407,3 +407,64 @@ def test_gates_alone(kind, dtype):
     for name, got, ref, lim in (("phi", phi, want, rel * want.abs()), ("phi'", d["dgate"], dwant, dabs),
                                 ("dy", d["dy"], want, rel * want.abs())):
         check(name, got, ref, lim + layer.TINY)
+
+
+@pytest.mark.parametrize("C", [4, 16])
+def test_around_the_lattice_layer(C):
+    """The chunked recurrence between the norms, and the scan as the next layer: recurrence (bf16 y) -> gated norm
+    of each head -> norm with the residual -> scan, and the gradients back through all of them.  Each call
+    against its own oracle on what the call before it wrote: the recurrence and its gradients at their bf16 bar
+    (2e-2 of the oracle's RMS), the norms and the scan element by element."""
+    import numpy as np
+
+    import oracle as osr_oracle
+    from compressed_memory_linear_amd import synth
+    from oracle import osr_backward
+
+    B, T, H, m, d = 2, 64, 2, 32, 64
+    D = H * d
+    inp = synth.make_inputs(B, T, H, m, d, seed=1400 + C)
+    t = osr.to_device(inp)
+    g = torch.Generator(device="cuda").manual_seed(C)
+    r = lambda *s, k=1.0, mean=0.0: torch.randn(s, generator=g, device="cuda") * k + mean
+    gate, x, f = r(B, T, H, d, k=1.5).to(BF), r(B, T, D).to(BF), r(B, T, D, mean=2.0).to(BF)
+    wh, w1, sc, w2 = r(d, k=0.2, mean=1), r(D, k=0.2, mean=1), r(D, k=0.1, mean=0.3), r(D, k=0.2, mean=1)
+    dxo, dh, dso = r(B, T, D).to(BF), r(B, T, D).to(BF), r(B, H, m, d)
+
+    args = [t[k] for k in ("q", "k", "v", "gamma", "mu", "state")]
+    y, S = osr.lattice_osr_fwd_chunked(*args, C, y_dtype=BF)
+    heads = dict(gate=gate, w_post=wh, pre_norm=False)
+    yh, _ = osr.lattice_osr_norm_fwd(y, **heads)
+    block = dict(w_post=w1, scale=sc, w_pre=w2)
+    yb = yh.view(B, T, D)
+    xo, z = osr.lattice_osr_norm_fwd(yb, x, **block)
+    h, _, saved = osr.lattice_osr_scan_fwd(z, f, y_dtype=BF, save=True)
+    g3 = osr.lattice_osr_scan_bwd(z, f, dh, saved=saved, grad_dtype=BF)
+    g2 = osr.lattice_osr_norm_bwd(yb, x, dxo, g3["dv"], grad_dtype=BF, **block)
+    g1 = osr.lattice_osr_norm_bwd(y, None, g2["dy"].view(B, T, H, d), grad_dtype=BF, **heads)
+    g0 = osr.lattice_osr_bwd_chunked(*args, g1["dy"], dso, C)
+    torch.cuda.synchronize()
+
+    def rms(name, got, ref):
+        err = float(np.max(np.abs(got.float().cpu().numpy() - ref)) / np.sqrt(np.mean(ref ** 2)))
+        print(f"  {name}: err/rms {err:.3e}", flush=True)
+        assert err <= 2e-2, (name, err)
+
+    yr, Sr = osr_oracle.osr_forward(*inp.values_f64(), chunk_size=C)
+    rms("y", y, yr)
+    rms("state", S, Sr)
+    ref = osr_backward.osr_backward(*inp.values_f64(), g1["dy"].float().cpu().numpy(), dso.cpu().numpy(), chunk_size=C)
+    for k in ref:
+        rms(k, g0[k], ref[k])
+
+    rows = lambda a: a.reshape(-1, a.shape[-1])
+    for got, out, names in (
+            ({**g1, "x_out": yh}, layer.norm(rows(y), None, rows(gate), post=True, w_post=wh, pre=False,
+                                             dx_out=g2["dy"].view(-1, d), backward=True),
+             ("x_out", "dy", "dgate", "dw_post")),
+            ({**g2, "x_out": xo, "z": z}, layer.norm(rows(yb), rows(x), None, post=True, w_post=w1, scale=sc, w_pre=w2,
+                                                     dx_out=rows(dxo), dz=rows(g3["dv"]), backward=True),
+             ("x_out", "z", "dy", "dx", "dw_post", "dscale", "dw_pre")),
+            ({**g3, "y": h}, layer.scan(z, f, dy=dh), ("y", "dv", "dmu_logit", "dstate_in"))):
+        for n in names:
+            check(n, got[n], out[0][n].view(got[n].shape), out[1][n].view(got[n].shape))
