@@ -12,8 +12,9 @@
 // order by a second kernel (no atomics: reruns agree bit for bit).
 //
 // Bound by HBM: R32768 D2048 bf16 with every operand moves 1.07 GB in 204 us, 5.3 TB/s (the
-// device's own copy of 1 GiB: 5.4); 82 vector operations per value keep the vector units 40 %
-// busy.  Rows of 64 values are bound by those operations (R65536: 15 us for 34 MB, 9 of them).
+// device's own copy of 1 GiB: 5.4); 75 vector operations per value keep the vector units 65 %
+// busy.  Rows of 64 values (R65536, SiLU, post-norm alone: 15 us for 34 MB) are bound by latency: 49 operations
+// per value are 5.4 us and the bytes 6.3, but a workgroup's rows are four steps of load, sums and store.
 #include "layer_norm.h"
 
 namespace layer {
@@ -218,14 +219,17 @@ __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     if (p.dw_pre) put_columns<S, VEC>(part + 2 * p.D, &cols[0][0], lane, sub, p.D, gpre);
 }
 
-// The same for wide rows, on 1024 threads of 128 registers each.  What does not fit them lies in
-// LDS, where every thread finds its own and no other's: the weights with one piece a thread,
+// The same for wide rows, on 1024 threads of 128 registers each.  Much of what does not fit them lies
+// in LDS, where every thread finds its own and no other's: the weights with one piece a thread,
 // two of the three column sums with two (the weights are then read from the cache).  No row is
-// loaded ahead, and the gates are taken twice.
+// loaded ahead, and the gates are taken twice.  Spilled all the same: nothing with one 16-byte piece a thread, 7 to 16
+// registers with eight single elements, 22 to 37 and 80 to 98 with two pieces of either.
 // R8192 D8192: bf16 252 us, 4.3 TB/s, fp32 467 us (the kernel above, spilling: 885 and 1946; this one
 // with the next row in flight, spilling: 298 and 737; with the weights from the cache too, 430
-// in bf16).  R4096 D16384 bf16: 479 us, 2.2 TB/s (2016; with every sum in registers 707).  Bound by latency: one
-// workgroup per compute unit, three sums over 16 waves per row, nothing else to run meanwhile.
+// in bf16).  R4096 D16384 bf16: 479 us, 2.2 TB/s (2016; with every sum in registers 707); R5461 D12288 559 us,
+// 1.9 TB/s.  Rows that do not fill the threads: R13107 D5120 bf16 321 us, 3.3 TB/s; element by element, R8192
+// D8190 334 us, 3.2.  Bound by latency: one workgroup per compute unit, three sums over 16 waves per
+// row, nothing else to run meanwhile.
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_wide_kernel(NormParams p) {
     constexpr bool kWeights = S::K == 1;  // in LDS

@@ -4,7 +4,10 @@
 //     z = x' / rms(x') w_pre,   rms(a) = sqrt(mean(a^2) + eps).
 // x' leaves rounded to its own type; z is taken from x' before that rounding.
 //
-// Bound by HBM: R32768 D2048 bf16 with every operand moves 671 MB in 114 us, 5.9 TB/s.
+// Bound by HBM: R32768 D2048 bf16 with every operand moves 671 MB in 114 us, 5.9 TB/s; R8192 D8192 128 us, 5.3;
+// R4096 D16384 124 us, 5.4.  Past 8192 values all but bf16 throughout spill 4 to 19 registers (fp32 R2048 D16384
+// 173 us, 3.9 TB/s), and single elements 49 or 50.  A decoding step's R256 D4096 (7 us for 13 MB) is one row per
+// workgroup: the latency of its loads and of two sums over eight waves, one after the other.
 #include "layer_norm.h"
 
 namespace layer {

@@ -14,9 +14,9 @@
 // more to form y.  Every input is read once and every output written once.
 //
 // Bound by HBM (bf16, D2048): B8 T4096 403 MB in 79 us, 5.1 TB/s; B1 T65536 with the writing
-// intensity 1.07 GB in 209 us, 5.1 TB/s (the device's own copy of 1 GiB: 5.4); about 19 vector
-// operations per element, two of the slow kind per gate, keep the vector units 45 % busy.  The kernel that
-// clears the hand-off words costs 3 to 5 us more.
+// intensity 1.07 GB in 209 us, 5.1 TB/s (the device's own copy of 1 GiB: 5.4); 18 vector
+// operations per element (24 with the intensity), two of the slow kind per gate, keep the vector units
+// 43 % busy.  The kernel that clears the hand-off words costs 3 to 5 us more.
 #include "layer_chain.h"
 #include "layer_device.h"
 #include "layer_launch.h"

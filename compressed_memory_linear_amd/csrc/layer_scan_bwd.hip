@@ -12,9 +12,12 @@
 // from the state the forward saved before it, and nothing else of the forward is kept.
 //
 // Bound by HBM and, with few chains, by the tiles' waits for one another (bf16, D2048): B8 T4096 with
-// the writing intensity 940 MB in 195 us, 4.8 TB/s; B1 T65536 without 1.34 GB in 273 us, 4.9 TB/s.
+// the writing intensity 940 MB in 187 to 209 us, 4.5 to 5.0 TB/s; B1 T65536 without 1.34 GB in 273
+// to 284 us, 4.7 to 4.9 TB/s.  The vector units are 47 and 43 % busy.
 // Runs of 16 tokens (126 registers with the intensity): 8 tokens 578 us for the latter's training
-// step, 16 428, 24 408, but 334, 306 and 336 for the former's.
+// step, 16 428, 24 408, but 334, 306 and 336 for the former's.  Weight 1 with the intensity holds both
+// gates' factors over the second pass and spills 10 to 18 registers: 205 us at B8 T4096 where
+// 1 - mu takes 193 and sqrt(1 - mu^2) 196.
 #include "layer_chain.h"
 #include "layer_device.h"
 #include "layer_launch.h"

@@ -434,9 +434,10 @@ LATTICE_OSR_API int lattice_osr_glue_post(const lattice_osr_desc* desc, const vo
  *                             outside [0, T] are taken as the nearer end.
  * mu_logit = -inf drops the state before a token (a document's border inside a
  * row), +inf keeps it; either has a zero gradient.  D up to 2^20, odd ones
- * included; element alignment only (rows move in wider pieces where D and the
- * addresses allow).  B ceil(D / 64) ceil(T / 128) must stay below 2^22, which
- * for one sequence of up to 64 channels means T up to 2^29 - 128.
+ * included; element alignment only (the single step moves four channels at a
+ * time where B D and the addresses allow).  B ceil(D / 64) ceil(T / 128) must
+ * stay below 2^22, which for one sequence of up to 64 channels means T up to
+ * 2^29 - 128.
  */
 #define LATTICE_OSR_SCAN_ONE 0        /* w = 1                  */
 #define LATTICE_OSR_SCAN_COMPLEMENT 1 /* w = 1 - mu             */
@@ -505,7 +506,8 @@ LATTICE_OSR_API size_t lattice_osr_scan_workspace_bytes(const lattice_osr_scan_d
  *   x, x_out             [R, D]  res_dtype
  *   w_post, scale, w_pre [D]     float32
  * D is at most 16384; element alignment (16-byte aligned rows with D a multiple
- * of 8 move in wider pieces).  eps must be a normal positive number.
+ * of 8 move in wider pieces).  eps must be a normal positive number.  Squares are
+ * summed in fp32: a row whose sum passes 3.4e38 counts as one of infinite rms.
  */
 #define LATTICE_OSR_GATE_NONE 0
 #define LATTICE_OSR_GATE_GELU 1

@@ -468,3 +468,15 @@ def test_around_the_lattice_layer(C):
             ({**g3, "y": h}, layer.scan(z, f, dy=dh), ("y", "dv", "dmu_logit", "dstate_in"))):
         for n in names:
             check(n, got[n], out[0][n].view(got[n].shape), out[1][n].view(got[n].shape))
+
+
+def test_rows_whose_squares_pass_fp32():
+    """Such a row counts as one of infinite rms: zeros behind its norm, finite, and nothing of it in other rows."""
+    t, o, _, _ = make(12, 264, F, F, seed=28)
+    t["x"][4] = 1e20
+    x_out, z = osr.lattice_osr_norm_fwd(**t, **o)
+    assert (z[4] == 0).all() and torch.isfinite(z).all() and torch.isfinite(x_out).all()
+    keep = torch.arange(12, device="cuda") != 4
+    out, bound = oracle(t, o)
+    check("z", z[keep], out["z"][keep], bound["z"][keep])
+    check("x_out", x_out, out["x_out"], bound["x_out"])
