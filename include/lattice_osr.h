@@ -433,7 +433,8 @@ LATTICE_OSR_API int lattice_osr_glue_post(const lattice_osr_desc* desc, const vo
  *                             token (state_in where there is none).  Values
  *                             outside [0, T] are taken as the nearer end.
  * mu_logit = -inf drops the state before a token (a document's border inside a
- * row), +inf keeps it; either has a zero gradient.  D up to 2^20, odd ones
+ * row), +inf keeps it; either has a zero gradient.  (A state that is infinite or
+ * NaN is not dropped: 0 times it is NaN.)  D up to 2^20, odd ones
  * included; element alignment only (the single step moves four channels at a
  * time where B D and the addresses allow).  B ceil(D / 64) ceil(T / 128) must
  * stay below 2^22, which for one sequence of up to 64 channels means T up to

@@ -480,3 +480,42 @@ def test_rows_whose_squares_pass_fp32():
     out, bound = oracle(t, o)
     check("z", z[keep], out["z"][keep], bound["z"][keep])
     check("x_out", x_out, out["x_out"], bound["x_out"])
+
+
+@pytest.mark.parametrize("kind", [osr.GATE_GELU, osr.GATE_SILU])
+@pytest.mark.parametrize("dtype", [F, BF])
+def test_gates_at_the_ends_of_the_type(kind, dtype):
+    """The lowest value closes a gate and the highest opens it, with derivatives 0 and 1, and nothing becomes NaN."""
+    big = torch.finfo(dtype).max
+    g = torch.tensor([-big, -big / 2, -1e30, -1e4, -200.0, 200.0, 1e4, 1e30, big / 2, big] * 2, device="cuda").to(dtype)
+    g = g.view(2, 10)
+    one = torch.ones_like(g)
+    phi, _ = osr.lattice_osr_norm_fwd(one, None, gate=g, gate_kind=kind, post_norm=False, pre_norm=False, x_dtype=F)
+    d = osr.lattice_osr_norm_bwd(one, None, one.float(), gate=g, gate_kind=kind, post_norm=False, pre_norm=False)
+    assert torch.equal(phi, torch.where(g > 0, g, 0).float()) and torch.equal(d["dy"], phi)
+    assert torch.equal(d["dgate"], (g > 0).float())
+
+
+@pytest.mark.parametrize("R,D", [(700, 64), (1300, 2048), (600, 5000), (600, 9001)])
+def test_outputs_that_are_not_wanted(R, D):
+    """The C calls without x_out, dx or some of the weights' gradients: the rest bit for bit, whatever is left out."""
+    import ctypes
+
+    t, o, dx_out, dz = make(R, D, BF, BF, seed=29)
+    desc = osr.make_norm_desc(R, D, osr.BF16, osr.BF16, osr.F32, o["gate_kind"])
+    lib, ref, ptr = osr.load_library(), ctypes.byref(desc), lambda a: None if a is None else a.data_ptr()
+    st = torch.cuda.current_stream().cuda_stream
+    ins = [ptr(t[k]) for k in ("y", "gate", "x", "w_post", "scale", "w_pre")]
+    x_out, z = osr.lattice_osr_norm_fwd(**t, **o)
+    z2 = torch.empty_like(z)
+    assert lib.lattice_osr_norm_fwd(ref, *ins, None, ptr(z2), st) == osr.OK
+    assert torch.equal(z, z2)
+    want = osr.lattice_osr_norm_bwd(**t, **o, dx_out=dx_out, dz=dz)
+    ws = torch.empty(osr.lattice_osr_norm_bwd_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    names = ("dy", "dgate", "dx", "dw_post", "dscale", "dw_pre")
+    for left in (("dx",), ("dw_post",), ("dscale",), ("dw_pre",), ("dw_post", "dscale"), ("dx", "dw_post", "dscale", "dw_pre")):
+        got = {k: None if k in left else torch.empty_like(want[k]) for k in names}
+        sums = any(got[k] is not None for k in names[3:])
+        assert lib.lattice_osr_norm_bwd(ref, *ins, ptr(dx_out), ptr(dz), *[ptr(got[k]) for k in names],
+                                        ptr(ws) if sums else None, ws.numel() if sums else 0, st) == osr.OK
+        assert all(got[k] is None or torch.equal(got[k], want[k]) for k in names), left

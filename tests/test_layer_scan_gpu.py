@@ -539,3 +539,30 @@ def test_infinite_states_stay_infinite_under_strong_forgetting(T, dtype):
         assert torch.equal(torch.isinf(g["dv"]), bad) and not torch.isnan(g["dv"]).any()
         assert torch.equal(torch.isinf(g["dstate_in"]), bad[:, 0])
         assert (g["dv"][0, :, 3] > 0).all() and (g["dv"][0, :, 5] < 0).all()
+
+
+@pytest.mark.parametrize("T", [1, 100, 700])
+def test_outputs_that_are_not_wanted(T):
+    """The C calls without state_out, saved, dstate_in: the rest bit for bit, whatever is left out."""
+    import ctypes
+
+    B, D = 3, 70
+    x = make(B, T, D, F, seed=94)
+    desc = osr.make_scan_desc(B, T, D, osr.F32, osr.F32, osr.F32)
+    lib, ref, ptr = osr.load_library(), ctypes.byref(desc), lambda t: None if t is None else t.data_ptr()
+    st = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(max(16, osr.lattice_osr_scan_workspace_bytes(desc)), dtype=torch.uint8, device="cuda")
+    y, so, sv = osr.lattice_osr_scan_fwd(x["v"], x["mu_logit"], x["state_in"], gamma_logit=x["gamma_logit"], save=True)
+    dy, dso = grads_of(B, T, D, F)
+    g = osr.lattice_osr_scan_bwd(x["v"], x["mu_logit"], dy, dso, saved=sv, gamma_logit=x["gamma_logit"])
+    for saved in (None, torch.zeros_like(sv)):
+        y2 = torch.empty_like(y)
+        assert lib.lattice_osr_scan_fwd(ref, ptr(x["v"]), ptr(x["mu_logit"]), ptr(x["gamma_logit"]), None,
+                                        ptr(x["state_in"]), None, ptr(y2), ptr(saved), sv.numel() if saved is not None
+                                        else 0, ptr(ws), ws.numel(), st) == osr.OK
+        assert torch.equal(y, y2) and (saved is None or torch.equal(saved, sv))
+    outs = [torch.empty_like(y) for _ in range(3)]
+    assert lib.lattice_osr_scan_bwd(ref, ptr(x["v"]), ptr(x["mu_logit"]), ptr(x["gamma_logit"]), None, ptr(sv),
+                                    sv.numel(), ptr(dy), ptr(dso), *[ptr(t) for t in outs], None, ptr(ws), ws.numel(),
+                                    st) == osr.OK
+    assert all(torch.equal(a, g[k]) for a, k in zip(outs, ("dv", "dmu_logit", "dgamma_logit")))
