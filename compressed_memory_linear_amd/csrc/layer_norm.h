@@ -164,6 +164,31 @@ __device__ __forceinline__ float rsqrt_acc(float x) {
     return r > 0.0f ? r * fmaf(-0.5f * x * r, r, 1.5f) : r;
 }
 
+// This workgroup's column sums g, into its row of the workspace.
+template <typename S, bool VEC>
+__device__ __forceinline__ void put_columns(float* to, float* cols, int lane, int sub, int D, const float (&g)[S::K][kE]) {
+    if constexpr (S::ROWS == 1) {
+#pragma unroll
+        for (int k = 0; k < S::K; ++k)
+#pragma unroll
+            for (int e = 0; e < kE; ++e) {
+                const int c = col_of<S, VEC>(lane, k, e);
+                if (c < D) to[c] = g[k][e];
+            }
+    } else {
+        constexpr int kCols = S::TPR * kE;  // the row slots' sums meet in LDS
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < kE; ++e) cols[sub * kCols + col_of<S, VEC>(lane, 0, e)] = g[0][e];
+        __syncthreads();
+        for (int c = threadIdx.x; c < D; c += S::NT) {
+            float s = 0.0f;
+            for (int i = 0; i < S::ROWS; ++i) s += cols[i * kCols + c];
+            to[c] = s;
+        }
+    }
+}
+
 // GeLU's parts for a gate g: cdf = Phi(g), and e = exp(-g^2 / 2), which its density takes too.
 // With a = |g| and t = 1 / (1 + 0.35 a), Phi(-a) = e t q(t): q is the polynomial of degree 8
 // nearest to exp(a^2 / 2) Phi(-a) / t in relative error (1.72e-7 for a up to 20, fitted for this by

@@ -67,31 +67,6 @@ __device__ __forceinline__ void gates(int kind, const Piece<TIn>& raw, float (&p
         for (int e = 0; e < kE; ++e) phi[e] = 1.0f, dphi[e] = 0.0f;
     }
 }
-// This workgroup's column sums g, into its row of the workspace.
-template <typename S, bool VEC>
-__device__ __forceinline__ void put_columns(float* to, float* cols, int lane, int sub, int D, const float (&g)[S::K][kE]) {
-    if constexpr (S::ROWS == 1) {
-#pragma unroll
-        for (int k = 0; k < S::K; ++k)
-#pragma unroll
-            for (int e = 0; e < kE; ++e) {
-                const int c = col_of<S, VEC>(lane, k, e);
-                if (c < D) to[c] = g[k][e];
-            }
-    } else {
-        constexpr int kCols = S::TPR * kE;  // the row slots' sums meet in LDS
-        __syncthreads();
-#pragma unroll
-        for (int e = 0; e < kE; ++e) cols[sub * kCols + col_of<S, VEC>(lane, 0, e)] = g[0][e];
-        __syncthreads();
-        for (int c = threadIdx.x; c < D; c += S::NT) {
-            float s = 0.0f;
-            for (int i = 0; i < S::ROWS; ++i) s += cols[i * kCols + c];
-            to[c] = s;
-        }
-    }
-}
-
 template <typename S, bool VEC, typename TIn, typename TRes>
 __global__ __launch_bounds__(S::NT) void layer_norm_bwd_kernel(NormParams p) {
     __shared__ float red[2][S::NT / 64][2];

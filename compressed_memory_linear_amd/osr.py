@@ -28,6 +28,7 @@ OVERLAP_AUTO, OVERLAP_OFF = 0, 1
 BWD_AUTO, BWD_WALK, BWD_CHUNK = 0, 1, 2
 SCAN_ONE, SCAN_COMPLEMENT, SCAN_NORM = 0, 1, 2
 GATE_NONE, GATE_GELU, GATE_SILU = 0, 1, 2
+CONV_NONE, CONV_SILU = 0, 1
 
 OK = 0
 ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_LAUNCH, ERR_ALIAS, ERR_ALIGN = -1, -2, -3, -4, -5, -6, -7
@@ -39,7 +40,11 @@ EXPORTED = ("lattice_osr_fwd_chunked", "lattice_osr_fwd_recurrent", "lattice_osr
             "lattice_osr_fwd_chunked_save", "lattice_osr_bwd_chunked_saved", "lattice_osr_scan_fwd",
             "lattice_osr_scan_bwd", "lattice_osr_scan_step", "lattice_osr_scan_saved_bytes",
             "lattice_osr_scan_workspace_bytes", "lattice_osr_norm_fwd", "lattice_osr_norm_bwd",
-            "lattice_osr_norm_bwd_workspace_bytes")
+            "lattice_osr_norm_bwd_workspace_bytes", "lattice_osr_conv_fwd", "lattice_osr_conv_bwd",
+            "lattice_osr_conv_step", "lattice_osr_conv_bwd_workspace_bytes", "lattice_osr_ssm_fwd",
+            "lattice_osr_ssm_bwd", "lattice_osr_ssm_step", "lattice_osr_ssm_saved_bytes",
+            "lattice_osr_ssm_workspace_bytes", "lattice_osr_ssm_bwd_workspace_bytes", "lattice_osr_layernorm_fwd",
+            "lattice_osr_layernorm_bwd", "lattice_osr_layernorm_bwd_workspace_bytes")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
@@ -56,6 +61,20 @@ class lattice_osr_scan_desc(ctypes.Structure):
 class lattice_osr_norm_desc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in
                 ("R", "D", "in_dtype", "res_dtype", "grad_dtype", "gate_kind", "post_norm", "pre_norm")] + \
+               [("eps", ctypes.c_float)]
+
+
+class lattice_osr_conv_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "W", "act", "in_dtype", "y_dtype", "grad_dtype", "x_row")]
+
+
+class lattice_osr_ssm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "D", "N", "G", "in_dtype", "y_dtype", "grad_dtype", "softplus",
+                                             "x_row", "dt_row", "z_row", "b_row", "c_row")]
+
+
+class lattice_osr_layernorm_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("R", "D", "in_dtype", "res_dtype", "grad_dtype")] + \
                [("eps", ctypes.c_float)]
 
 
@@ -109,7 +128,22 @@ def load_library():
         lib.lattice_osr_norm_bwd.argtypes = [np_] + [vp] * 15 + [sz, vp]
         for f in ("scan_fwd", "scan_bwd", "scan_step", "norm_fwd", "norm_bwd"):
             getattr(lib, "lattice_osr_" + f).restype = ctypes.c_int
-        for f, d in (("scan_saved_bytes", sp), ("scan_workspace_bytes", sp), ("norm_bwd_workspace_bytes", np_)):
+        cp, mp, lp = (ctypes.POINTER(d) for d in (lattice_osr_conv_desc, lattice_osr_ssm_desc,
+                                                  lattice_osr_layernorm_desc))
+        lib.lattice_osr_conv_fwd.argtypes = [cp] + [vp] * 9
+        lib.lattice_osr_conv_bwd.argtypes = [cp] + [vp] * 13 + [sz, vp]
+        lib.lattice_osr_conv_step.argtypes = [cp] + [vp] * 7
+        lib.lattice_osr_ssm_fwd.argtypes = [mp] + [vp] * 14 + [sz, vp, sz, vp]
+        lib.lattice_osr_ssm_bwd.argtypes = [mp] + [vp] * 11 + [sz] + [vp] * 12 + [sz, vp]
+        lib.lattice_osr_ssm_step.argtypes = [mp] + [vp] * 12
+        lib.lattice_osr_layernorm_fwd.argtypes = [lp] + [vp] * 7
+        lib.lattice_osr_layernorm_bwd.argtypes = [lp] + [vp] * 10 + [sz, vp]
+        for f in ("conv_fwd", "conv_bwd", "conv_step", "ssm_fwd", "ssm_bwd", "ssm_step", "layernorm_fwd",
+                  "layernorm_bwd"):
+            getattr(lib, "lattice_osr_" + f).restype = ctypes.c_int
+        for f, d in (("conv_bwd_workspace_bytes", cp), ("ssm_saved_bytes", mp), ("ssm_workspace_bytes", mp),
+                     ("ssm_bwd_workspace_bytes", mp), ("layernorm_bwd_workspace_bytes", lp),
+                     ("scan_saved_bytes", sp), ("scan_workspace_bytes", sp), ("norm_bwd_workspace_bytes", np_)):
             getattr(lib, "lattice_osr_" + f).argtypes = [d]
             getattr(lib, "lattice_osr_" + f).restype = sz
         lib.lattice_osr_status_string.argtypes = [ctypes.c_int]
@@ -850,6 +884,452 @@ def lattice_osr_norm_bwd(y=None, x=None, dx_out=None, dz=None, *, gate=None, gat
                                       _ptr(g.get("dw_pre")), _ptr(ws), wbytes, st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_norm_bwd")
+        return g
+
+    return _on(dev, stream, call)
+
+
+# -------------------------------------- selective state space layer --
+def _row(name, t, shape, dtype, dev, inner):
+    """Elements from one token's row of t to the next (0: contiguous), after checking its shape, dtype and
+    device: t is [B,T,...] whose last `inner` dimensions are contiguous and whose rows
+    are one stride apart, as a slice of the last dimension of a contiguous tensor is."""
+    if t.is_contiguous():
+        _check_tensor(name, t, shape, dtype, dev)
+        return 0
+    if tuple(t.shape) != tuple(shape):
+        _shape_error(name, t, shape)
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, expected {dtype}")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, expected {dev}")
+    width = 1
+    for k in range(t.dim() - 1, t.dim() - 1 - inner, -1):
+        if t.shape[k] != 1 and t.stride(k) != width:
+            raise ValueError(f"{name} must be contiguous but for the stride between tokens")
+        width *= t.shape[k]
+    B, T = t.shape[:2]
+    row = t.stride(1) if T > 1 else t.stride(0)
+    if B > 1 and t.stride(0) != T * row or not width <= row < 2 ** 31:
+        raise ValueError(f"{name} must be contiguous but for the stride between tokens")
+    return row
+
+
+def _lead(name, x):
+    """(B, T, D, shape of one token) of a [B,T,D] or [B,T,H,d] tensor."""
+    if x.dim() not in (3, 4):
+        raise ValueError(f"{name} is [B,T,D] or [B,T,H,d]")
+    if x.dtype not in _DT:
+        raise ValueError("inputs must be float32 or bfloat16")
+    D = x.shape[2] if x.dim() == 3 else x.shape[2] * x.shape[3]
+    if max(x.shape[0], x.shape[1], D) > 2 ** 31 - 1:
+        raise ValueError(f"shape {tuple(x.shape)}: sizes are at most 2^31 - 1")
+    return x.shape[0], x.shape[1], D, tuple(x.shape[2:])
+
+
+def _check_tokens(lengths, segments, B, T, dev):
+    if lengths is not None:
+        _check_tensor("lengths", lengths, (B,), torch.int32, dev)
+    if segments is not None:
+        _check_tensor("segments", segments, (B, T), torch.int32, dev)
+
+
+def _check_dtypes(*dtypes):
+    for dt in dtypes:
+        if dt not in _DT:
+            raise ValueError("tensors must be float32 or bfloat16")
+
+
+def make_conv_desc(B, T, D, W, act=CONV_SILU, in_dtype=BF16, y_dtype=BF16, grad_dtype=F32, x_row=0):
+    return lattice_osr_conv_desc(B, T, D, W, act, in_dtype, y_dtype, grad_dtype, x_row)
+
+
+def lattice_osr_conv_bwd_workspace_bytes(desc: lattice_osr_conv_desc) -> int:
+    return _bytes_of("lattice_osr_conv_bwd_workspace_bytes", desc)
+
+
+def _conv_desc(x, w, bias, hist_in, act, lengths, segments, y_dtype, grad_dtype):
+    """Descriptor fields of a convolution call, after checking every input against them."""
+    B, T, D, tok = _lead("x", x)
+    _check_dtypes(y_dtype, grad_dtype)
+    dev = x.device
+    if w.dim() != x.dim() - 1:
+        raise ValueError("w is [D,W], or [H,d,W] beside x [B,T,H,d]")
+    W = w.shape[-1]
+    _check_tensor("w", w, tok + (W,), torch.float32, dev)
+    if bias is not None:
+        _check_tensor("bias", bias, tok, torch.float32, dev)
+    row = _row("x", x, x.shape, None, None, len(tok))
+    hshape = (B, W - 1) + tok
+    if hist_in is not None:
+        _check_tensor("hist_in", hist_in, hshape, x.dtype, dev)
+    _check_tokens(lengths, segments, B, T, dev)
+    return (B, T, D, W, act, _DT[x.dtype], _DT[y_dtype], _DT[grad_dtype], row), hshape
+
+
+def lattice_osr_conv_fwd(x, w, bias=None, hist_in=None, *, act: int = CONV_SILU, lengths=None, segments=None,
+                         y_dtype=None, y=None, hist_out=None, return_history: bool = False, stream=None):
+    """p_t = bias + sum_j w[j] x_{t-W+1+j} per channel, y = p sigmoid(p) (act CONV_SILU) or p (CONV_NONE).
+
+    x [B,T,D] or [B,T,H,d] (float32 or bfloat16; its rows may be a stride apart, as in a slice of a
+    projection's output), w [D,W] and bias [D] float32; hist_in [B,W-1,D] in x's dtype, the raw rows before
+    the first token (None: zeros); lengths [B] int32: the tokens of each sequence, y is zero behind them; segments
+    [B,T] int32: the document of every token, whose border no tap crosses.  y has x's shape, in y_dtype (x's
+    dtype if None).  Returns y and, with return_history (or `hist_out`), the raw rows behind the last
+    token, for the next call."""
+    lib = load_library()
+    y_dtype = x.dtype if y_dtype is None else y_dtype
+    fields, hshape = _conv_desc(x, w, bias, hist_in, act, lengths, segments, y_dtype, torch.float32)
+    dev = x.device
+    if y is not None:
+        _check_tensor("y", y, x.shape, y_dtype, dev)
+    if hist_out is not None:
+        _check_tensor("hist_out", hist_out, hshape, x.dtype, dev)
+    _check_cuda(x)
+    history = return_history or hist_out is not None
+
+    def call(st):
+        yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
+        ho = x.new_empty(hshape) if hist_out is None and history else hist_out
+        desc = lattice_osr_conv_desc(*fields)
+        rc = lib.lattice_osr_conv_fwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
+                                      _ptr(hist_in), _ptr(ho), _ptr(yy), st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_conv_fwd")
+        return (yy, ho) if history else yy
+
+    return _on(dev, stream, call)
+
+
+@functools.lru_cache(maxsize=1024)
+def _conv_size(fields):
+    return _query("lattice_osr_conv_bwd_workspace_bytes", lattice_osr_conv_desc(*fields)) or 0
+
+
+def lattice_osr_conv_bwd(x, w, dy, bias=None, hist_in=None, dhist_out=None, *, act: int = CONV_SILU, lengths=None,
+                         segments=None, grad_dtype=torch.float32, grads: Optional[dict] = None, workspace=None,
+                         stream=None) -> dict:
+    """Gradients of sum(dy*y) + sum(dhist_out*hist_out) of lattice_osr_conv_fwd with the same inputs.  dy has
+    x's shape (float32 or bfloat16), dhist_out the history's in grad_dtype (None: zeros).  Returns a dict of dx,
+    dhist_in (grad_dtype; the latter with hist_in), dw and dbias (float32; the latter with bias), allocated
+    unless passed in `grads`."""
+    lib = load_library()
+    fields, hshape = _conv_desc(x, w, bias, hist_in, act, lengths, segments, dy.dtype, grad_dtype)
+    dev = x.device
+    _check_tensor("dy", dy, x.shape, None, dev)
+    if dhist_out is not None:
+        _check_tensor("dhist_out", dhist_out, hshape, grad_dtype, dev)
+    f32 = torch.float32
+    want = [("dx", None, x.shape, grad_dtype), ("dw", None, w.shape, f32)]
+    if bias is not None:
+        want.append(("dbias", None, bias.shape, f32))
+    if hist_in is not None:
+        want.append(("dhist_in", None, hshape, grad_dtype))
+    _check_grads(grads, want, dev)
+    _check_cuda(x)
+
+    def call(st):
+        g = _grads(grads, want, x)
+        ws, wbytes = _room(workspace, _conv_size(fields), x)
+        desc = lattice_osr_conv_desc(*fields)
+        rc = lib.lattice_osr_conv_bwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
+                                      _ptr(hist_in), _ptr(dy), _ptr(dhist_out), _ptr(g["dx"]), _ptr(g["dw"]),
+                                      _ptr(g.get("dbias")), _ptr(g.get("dhist_in")), _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_conv_bwd")
+        return g
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_conv_step(x, w, hist_in, bias=None, *, act: int = CONV_SILU, y_dtype=None, y=None, hist_out=None,
+                          stream=None):
+    """One token of lattice_osr_conv_fwd (T = 1) for every sequence; hist_out may be hist_in (in place).
+    Returns (y, hist_out)."""
+    lib = load_library()
+    y_dtype = x.dtype if y_dtype is None else y_dtype
+    if hist_in is None:
+        raise ValueError("hist_in: the history of every sequence (zeros at its start)")
+    fields, hshape = _conv_desc(x, w, bias, hist_in, act, None, None, y_dtype, torch.float32)
+    dev = x.device
+    if y is not None:
+        _check_tensor("y", y, x.shape, y_dtype, dev)
+    if hist_out is not None:
+        _check_tensor("hist_out", hist_out, hshape, x.dtype, dev)
+    _check_cuda(x)
+
+    def call(st):
+        yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
+        ho = torch.empty_like(hist_in) if hist_out is None else hist_out
+        desc = lattice_osr_conv_desc(*fields)
+        rc = lib.lattice_osr_conv_step(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(hist_in), _ptr(ho),
+                                       _ptr(yy), st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_conv_step")
+        return yy, ho
+
+    return _on(dev, stream, call)
+
+
+def make_ssm_desc(B, T, D, N, G=1, in_dtype=BF16, y_dtype=BF16, grad_dtype=F32, softplus=1, x_row=0, dt_row=0, z_row=0,
+                  b_row=0, c_row=0):
+    return lattice_osr_ssm_desc(B, T, D, N, G, in_dtype, y_dtype, grad_dtype, softplus, x_row, dt_row, z_row, b_row,
+                                c_row)
+
+
+def lattice_osr_ssm_saved_bytes(desc: lattice_osr_ssm_desc) -> int:
+    return _bytes_of("lattice_osr_ssm_saved_bytes", desc)
+
+
+def lattice_osr_ssm_workspace_bytes(desc: lattice_osr_ssm_desc) -> int:
+    return _bytes_of("lattice_osr_ssm_workspace_bytes", desc)
+
+
+def lattice_osr_ssm_bwd_workspace_bytes(desc: lattice_osr_ssm_desc) -> int:
+    return _bytes_of("lattice_osr_ssm_bwd_workspace_bytes", desc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _ssm_sizes(fields):
+    """(saved, forward's workspace, backward's workspace) bytes; zeros for a descriptor that the call itself
+    refuses, with its status."""
+    desc = lattice_osr_ssm_desc(*fields)
+    return tuple(_query("lattice_osr_ssm_" + f, desc) or 0 for f in ("saved_bytes", "workspace_bytes",
+                                                                    "bwd_workspace_bytes"))
+
+
+def _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, segments, y_dtype, grad_dtype):
+    """Descriptor fields of a state space call and its state's shape, after checking every input against them."""
+    nb, T, ch, tok = _lead("x", x)
+    _check_dtypes(y_dtype, grad_dtype)
+    dev, dtype = x.device, x.dtype
+    if A.dim() != x.dim() - 1:
+        raise ValueError("A is [D,N], or [H,d,N] beside x [B,T,H,d]")
+    N = A.shape[-1]
+    _check_tensor("A", A, tok + (N,), torch.float32, dev)
+    for name, t in (("D", D), ("dt_bias", dt_bias)):
+        if t is not None:
+            _check_tensor(name, t, tok, torch.float32, dev)
+    k = len(tok)
+    rows = [_row("x", x, x.shape, None, None, k), _row("dt", dt, x.shape, dtype, dev, k),
+            _row("z", z, x.shape, dtype, dev, k) if z is not None else 0]
+    if B.dim() not in (3, 4):
+        raise ValueError("B and C are [B,T,N] or [B,T,G,N]")
+    G = B.shape[2] if B.dim() == 4 else 1
+    shape = (nb, T, G, N) if B.dim() == 4 else (nb, T, N)
+    rows += [_row("B", B, shape, dtype, dev, len(shape) - 2), _row("C", C, shape, dtype, dev, len(shape) - 2)]
+    _check_tokens(lengths, segments, nb, T, dev)
+    fields = (nb, T, ch, N, G, _DT[dtype], _DT[y_dtype], _DT[grad_dtype], int(softplus), *rows)
+    return fields, (nb,) + tok + (N,)
+
+
+def lattice_osr_ssm_fwd(x, dt, A, B, C, state_in=None, *, D=None, z=None, dt_bias=None, softplus: bool = True,
+                        lengths=None, segments=None, y_dtype=torch.float32, y=None, state_out=None, save: bool = False,
+                        saved=None, workspace=None, stream=None):
+    """h_t = exp(delta_t A) h_{t-1} + delta_t x_t B_t per channel and state, delta = softplus(dt + dt_bias) (or the
+    sum itself), y_t = (sum_n C_t h_t + D x_t) z_t sigmoid(z_t) (no gate without z).
+
+    x, dt, z [B,T,D] or [B,T,H,d] and B, C [B,T,N] or [B,T,G,N] (channel c takes group c // (D/G)) share a
+    dtype, float32 or bfloat16; rows may be a stride apart, as in a slice of a projection's output.  A [D,N],
+    D and dt_bias [D] are float32, state_in (None: zeros) and state_out [B,D,N] too, state_out may be
+    state_in; lengths [B] int32: the tokens of each sequence, y is zero behind them; segments [B,T] int32: the
+    document of every token, at whose borders the state starts from zero.
+    Returns (y, state_out) and, with save (or `saved`, a uint8 tensor of lattice_osr_ssm_saved_bytes), what
+    lattice_osr_ssm_bwd needs."""
+    lib = load_library()
+    fields, sshape = _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, segments, y_dtype, torch.float32)
+    dev = x.device
+    for name, t in (("state_in", state_in), ("state_out", state_out)):
+        if t is not None:
+            _check_tensor(name, t, sshape, torch.float32, dev)
+    if y is not None:
+        _check_tensor("y", y, x.shape, y_dtype, dev)
+    _check_cuda(x)
+    save = save or saved is not None
+
+    def call(st):
+        yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
+        so = x.new_empty(sshape, dtype=torch.float32) if state_out is None else state_out
+        snb, wnb, _ = _ssm_sizes(fields)
+        sv, sbytes = _room(saved, snb, x) if save else (None, 0)
+        ws, wbytes = _room(workspace, wnb, x)
+        desc = lattice_osr_ssm_desc(*fields)
+        rc = lib.lattice_osr_ssm_fwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                     _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(state_in), _ptr(so), _ptr(yy),
+                                     _ptr(sv), sbytes, _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_ssm_fwd")
+        return (yy, so, sv) if save else (yy, so)
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_ssm_bwd(x, dt, A, B, C, dy, dstate_out=None, *, saved, D=None, z=None, dt_bias=None,
+                        softplus: bool = True, lengths=None, segments=None, grad_dtype=torch.float32,
+                        grads: Optional[dict] = None, workspace=None, stream=None) -> dict:
+    """Gradients of sum(dy*y) + sum(dstate_out*state_out) of lattice_osr_ssm_fwd with the same inputs, whose
+    `saved` this call takes.  dy has x's shape (float32 or bfloat16), dstate_out the state's (None: zeros).
+    Returns a dict of dx, ddt, dB, dC (and dz, with z) in grad_dtype, and dA, dstate_in (dD with D, ddt_bias
+    with dt_bias) in float32, allocated unless passed in `grads`."""
+    lib = load_library()
+    if saved is None:
+        raise ValueError("saved: the tensor lattice_osr_ssm_fwd returned with save=True")
+    fields, sshape = _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, segments, dy.dtype, grad_dtype)
+    dev = x.device
+    _check_tensor("dy", dy, x.shape, None, dev)
+    if dstate_out is not None:
+        _check_tensor("dstate_out", dstate_out, sshape, torch.float32, dev)
+    f32 = torch.float32
+    want = [(n, None, t.shape, dt_) for n, t, dt_ in (("dx", x, grad_dtype), ("ddt", x, grad_dtype), ("dA", A, f32),
+                                                     ("dB", B, grad_dtype), ("dC", C, grad_dtype), ("dD", D, f32),
+                                                     ("dz", z, grad_dtype), ("ddt_bias", dt_bias, f32))
+            if t is not None]
+    want.append(("dstate_in", None, sshape, f32))
+    _check_grads(grads, want, dev)
+    _check_cuda(x)
+
+    def call(st):
+        g = _grads(grads, want, x)
+        sv, sbytes = _workspace(saved, 0, dev)
+        ws, wbytes = _room(workspace, _ssm_sizes(fields)[2], x)
+        desc = lattice_osr_ssm_desc(*fields)
+        rc = lib.lattice_osr_ssm_bwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+                                     _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(sv), sbytes, _ptr(dy),
+                                     _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]),
+                                     _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")), _ptr(g.get("ddt_bias")),
+                                     _ptr(g["dstate_in"]), _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_ssm_bwd")
+        return g
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_ssm_step(x, dt, A, B, C, state_in, *, D=None, z=None, dt_bias=None, softplus: bool = True,
+                         y_dtype=torch.float32, y=None, state_out=None, stream=None):
+    """One token of lattice_osr_ssm_fwd (T = 1) for every sequence; state_out may be state_in (in place).
+    Returns (y, state_out)."""
+    lib = load_library()
+    fields, sshape = _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, None, None, y_dtype, torch.float32)
+    dev = x.device
+    _check_tensor("state_in", state_in, sshape, torch.float32, dev)
+    if state_out is not None:
+        _check_tensor("state_out", state_out, sshape, torch.float32, dev)
+    if y is not None:
+        _check_tensor("y", y, x.shape, y_dtype, dev)
+    _check_cuda(x)
+
+    def call(st):
+        yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
+        so = torch.empty_like(state_in) if state_out is None else state_out
+        desc = lattice_osr_ssm_desc(*fields)
+        rc = lib.lattice_osr_ssm_step(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+                                      _ptr(z), _ptr(dt_bias), _ptr(state_in), _ptr(so), _ptr(yy), st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_ssm_step")
+        return yy, so
+
+    return _on(dev, stream, call)
+
+
+def make_layernorm_desc(R, D, in_dtype=BF16, res_dtype=BF16, grad_dtype=F32, eps=1e-5):
+    return lattice_osr_layernorm_desc(R, D, in_dtype, res_dtype, grad_dtype, eps)
+
+
+def lattice_osr_layernorm_bwd_workspace_bytes(desc: lattice_osr_layernorm_desc) -> int:
+    return _bytes_of("lattice_osr_layernorm_bwd_workspace_bytes", desc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _layernorm_size(fields):
+    return _query("lattice_osr_layernorm_bwd_workspace_bytes", lattice_osr_layernorm_desc(*fields)) or 0
+
+
+def _layernorm_desc(x, y, w, b, in_dtype, grad_dtype, eps):
+    """Descriptor fields of a layer norm call, after checking every input against them."""
+    if x.dim() < 1:
+        raise ValueError("x and y are [..., D]")
+    _check_dtypes(x.dtype, in_dtype, grad_dtype)
+    dev, D = x.device, x.shape[-1]
+    _check_tensor("x", x, x.shape, None)
+    if y is not None:
+        _check_tensor("y", y, x.shape, in_dtype, dev)
+    for name, t in (("w", w), ("b", b)):
+        if t is not None:
+            _check_tensor(name, t, (D,), torch.float32, dev)
+    R = x.numel() // D if D else 0
+    if R > 2 ** 31 - 1:
+        raise ValueError(f"{R} rows: at most 2^31 - 1")
+    return R, D, _DT[in_dtype], _DT[x.dtype], _DT[grad_dtype], eps
+
+
+def lattice_osr_layernorm_fwd(x, y=None, *, w=None, b=None, eps: float = 1e-5, z_dtype=None, x_out=None, z=None,
+                              stream=None):
+    """x_out = x + y (y None: x itself), z = (x_out - mean) / sqrt(var + eps) w + b over the last dimension.
+
+    x [..., D] and y [..., D] have their own dtypes (float32 or bfloat16), z has y's (without y z_dtype, or
+    x's if that is None); w, b are [D] float32 (None: ones, zeros).  x_out has x's dtype and may be x (in place).
+    Returns (x_out, z); x_out is None without y."""
+    lib = load_library()
+    in_dtype = y.dtype if y is not None else z_dtype or x.dtype
+    if z_dtype is not None and z_dtype != in_dtype:
+        raise ValueError("z_dtype is y's dtype")
+    fields = _layernorm_desc(x, y, w, b, in_dtype, torch.float32, eps)
+    dev = x.device
+    if x_out is not None:
+        _check_tensor("x_out", x_out, x.shape, x.dtype, dev)
+    if z is not None:
+        _check_tensor("z", z, x.shape, in_dtype, dev)
+    _check_cuda(x)
+
+    def call(st):
+        xo = torch.empty_like(x) if x_out is None and y is not None else x_out
+        zz = torch.empty_like(x, dtype=in_dtype) if z is None else z
+        desc = lattice_osr_layernorm_desc(*fields)
+        rc = lib.lattice_osr_layernorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(w), _ptr(b), _ptr(xo), _ptr(zz),
+                                           st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_layernorm_fwd")
+        return xo, zz
+
+    return _on(dev, stream, call)
+
+
+def lattice_osr_layernorm_bwd(x, y=None, dx_out=None, dz=None, *, w=None, b=None, eps: float = 1e-5, grad_dtype=None,
+                              grads: Optional[dict] = None, workspace=None, stream=None) -> dict:
+    """Gradients of sum(dx_out*x_out) + sum(dz*z) of lattice_osr_layernorm_fwd with the same inputs.  dx_out (x's
+    dtype; None: zeros) and dz (y's dtype) have x's shape.  Returns a dict of dx (x's dtype), dy with y (grad_dtype, y's dtype
+    if that is None; dx itself where that is x's dtype), dw and db (float32, where w and b were passed),
+    allocated unless passed in `grads` (dx may be dx_out)."""
+    lib = load_library()
+    if dz is None:
+        raise ValueError("dz: the gradient of z")
+    in_dtype = y.dtype if y is not None else dz.dtype
+    grad_dtype = in_dtype if grad_dtype is None else grad_dtype
+    fields = _layernorm_desc(x, y, w, b, in_dtype, grad_dtype, eps)
+    dev = x.device
+    for name, t, dt in (("dx_out", dx_out, x.dtype), ("dz", dz, in_dtype)):
+        if t is not None:
+            _check_tensor(name, t, x.shape, dt, dev)
+    f32 = torch.float32
+    own_dy = y is not None and grad_dtype != x.dtype
+    want = [(n, t, t.shape, dt) for n, t, dt in (("dx", x, x.dtype), ("dy", y if own_dy else None, grad_dtype),
+                                                 ("dw", w, f32), ("db", b, f32)) if t is not None]
+    _check_grads(grads, want, dev)
+    _check_cuda(x)
+
+    def call(st):
+        g = _grads(grads, want, x)
+        sums = w is not None or b is not None
+        ws, wbytes = _room(workspace, _layernorm_size(fields) if sums else 0, x)
+        desc = lattice_osr_layernorm_desc(*fields)
+        rc = lib.lattice_osr_layernorm_bwd(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(w), _ptr(dx_out), _ptr(dz),
+                                           _ptr(g["dx"]), _ptr(g.get("dy")), _ptr(g.get("dw")), _ptr(g.get("db")),
+                                           _ptr(ws), wbytes, st)
+        if rc != OK:
+            raise OSRError(rc, "lattice_osr_layernorm_bwd")
+        if y is not None and not own_dy:
+            g["dy"] = g["dx"]
         return g
 
     return _on(dev, stream, call)

@@ -556,6 +556,194 @@ LATTICE_OSR_API int lattice_osr_norm_bwd(const lattice_osr_norm_desc* desc, cons
                                          size_t workspace_bytes, void* hip_stream);
 LATTICE_OSR_API size_t lattice_osr_norm_bwd_workspace_bytes(const lattice_osr_norm_desc* desc);
 
+/*
+ * Short causal convolution in front of a recurrence: depthwise along T, one
+ * filter per channel, with an activation,
+ *   p_t = bias[c] + sum_j w[c,j] x_{t-W+1+j},  j = 0 .. W-1,   y_t = act(p_t)
+ * (w[W-1] weighs the current token).  The rows before t = 0 are hist_in
+ * (zeros where it is NULL: sequence start).  Arithmetic is fp32.
+ *   x                  [B, T, D]      in_dtype, rows x_row apart
+ *   w                  [D, W]         float32;  bias [D] float32, or NULL
+ *   hist_in, hist_out  [B, W-1, D]    in_dtype, the raw rows before the call's
+ *                                     first and behind its last token, oldest first
+ *   y                  [B, T, D]      y_dtype
+ *   lengths            [B] int32, or NULL: as for the scan; y is zero at padding,
+ *                      hist_out ends with the last token (hist_in where there is none)
+ *   segments           [B, T] int32, or NULL: the document of every token.  A tap
+ *                      that lies before the last border (a token whose number
+ *                      differs from the one's before) reads zero; hist_in belongs
+ *                      to the first token's document, and rows of hist_out that lie before the
+ *                      last token's document are zeros.
+ * W is 1 to 8 (1: no history, whose buffers are then not used), D up to 2^20.
+ */
+#define LATTICE_OSR_CONV_NONE 0
+#define LATTICE_OSR_CONV_SILU 1
+#define LATTICE_OSR_CONV_MAX_W 8
+
+typedef struct {
+    int32_t B;          /* sequences                                          */
+    int32_t T;          /* tokens per sequence                                */
+    int32_t D;          /* channels                                           */
+    int32_t W;          /* taps                                               */
+    int32_t act;        /* LATTICE_OSR_CONV_NONE or _SILU                     */
+    int32_t in_dtype;   /* of x and the histories                             */
+    int32_t y_dtype;    /* of y and dy                                        */
+    int32_t grad_dtype; /* of dx, dhist_in and dhist_out                      */
+    int32_t x_row;      /* elements from one token's x to the next (sequences T
+                           rows apart), at least D; 0: D.  At most 2^22.       */
+} lattice_osr_conv_desc;
+
+/* Forward.  hist_in NULL: zeros; hist_out NULL: not wanted.  No output may overlap an argument (ERR_ALIAS).
+ * Element alignment only (16-byte aligned rows and buffers with D and x_row multiples of 8 move in wider pieces). */
+LATTICE_OSR_API int lattice_osr_conv_fwd(const lattice_osr_conv_desc* desc, const void* x, const float* w,
+                                         const float* bias, const int32_t* lengths, const int32_t* segments,
+                                         const void* hist_in, void* hist_out, void* y, void* hip_stream);
+
+/*
+ * Backward: the gradient of L = sum(dy * y) + sum(dhist_out * hist_out), with
+ * the forward's inputs (its outputs are not needed).
+ *   dy  [B, T, D] y_dtype;  dhist_out [B, W-1, D] grad_dtype, or NULL (zeros)
+ *   dx  [B, T, D] grad_dtype, contiguous, written in full (zeros at padding)
+ *   dw  [D, W], dbias [D]  float32, each NULL where it is not wanted
+ *   dhist_in  [B, W-1, D] grad_dtype, or NULL (not wanted)
+ * workspace: lattice_osr_conv_bwd_workspace_bytes(desc) bytes, 16-byte aligned (NULL
+ * allowed without dw and dbias).  The sums over tokens have a fixed order: reruns agree bit for bit.
+ */
+LATTICE_OSR_API int lattice_osr_conv_bwd(const lattice_osr_conv_desc* desc, const void* x, const float* w,
+                                         const float* bias, const int32_t* lengths, const int32_t* segments,
+                                         const void* hist_in, const void* dy, const void* dhist_out, void* dx,
+                                         float* dw, float* dbias, void* dhist_in, void* workspace,
+                                         size_t workspace_bytes, void* hip_stream);
+
+/* One token for each of B sequences (desc->T must be 1, W at least 2); hist_out may be hist_in itself (in place). */
+LATTICE_OSR_API int lattice_osr_conv_step(const lattice_osr_conv_desc* desc, const void* x, const float* w,
+                                          const float* bias, const void* hist_in, void* hist_out, void* y,
+                                          void* hip_stream);
+LATTICE_OSR_API size_t lattice_osr_conv_bwd_workspace_bytes(const lattice_osr_conv_desc* desc);
+
+/*
+ * Selective state space scan: per channel c, a state of N values,
+ *   delta = softplus(dt + dt_bias[c])   (softplus = 1; else dt + dt_bias[c]),
+ *   h_t[n] = exp(delta_t A[c,n]) h_{t-1}[n] + delta_t x_t B_t[n],
+ *   y_t = (sum_n C_t[n] h_t[n] + skip[c] x_t) z_t sigmoid(z_t)
+ * (no gate where z is NULL; skip, dt_bias NULL: zeros).  h_{-1} is state_in
+ * (zeros where it is NULL).  Steps, decays, states and sums are fp32.
+ *   x, dt, z        [B, T, D]     in_dtype, rows x_row, dt_row, z_row apart
+ *   Bm, Cm          [B, T, G, N]  in_dtype, rows b_row, c_row apart; channel c
+ *                                 takes group c / (D / G)
+ *   A               [D, N]        float32;  skip, dt_bias [D] float32
+ *   y               [B, T, D]     y_dtype
+ *   state_in/out    [B, D, N]     float32
+ *   lengths         [B] int32, or NULL: as for the element-wise scan
+ *   segments        [B, T] int32, or NULL: the document of every token; a token
+ *                   whose number differs from the one's before starts from a
+ *                   state of zeros, whatever the state was (the first token
+ *                   goes on from state_in)
+ * N is 1 to 64, D up to 2^20, G divides D, row strides up to 2^22; element
+ * alignment only.  B G ceil(D / (64 G)) must stay below 2^22.
+ */
+#define LATTICE_OSR_SSM_MAX_N 64
+
+typedef struct {
+    int32_t B;          /* sequences                                          */
+    int32_t T;          /* tokens per sequence                                */
+    int32_t D;          /* channels                                           */
+    int32_t N;          /* values of a channel's state                        */
+    int32_t G;          /* groups of channels that share B and C              */
+    int32_t in_dtype;   /* of x, dt, z, Bm, Cm                                */
+    int32_t y_dtype;    /* of y and dy                                        */
+    int32_t grad_dtype; /* of dx, ddt, dz, dB, dC                             */
+    int32_t softplus;   /* 1: delta = softplus(dt + dt_bias); 0: the sum      */
+    /* elements from one token's row to the next (sequences T rows apart); 0: contiguous */
+    int32_t x_row, dt_row, z_row, b_row, c_row;
+} lattice_osr_ssm_desc;
+
+/*
+ * Forward.  state_out may be NULL (not wanted) or state_in itself; no other
+ * output may overlap an argument.  saved, where not NULL, receives what
+ * lattice_osr_ssm_bwd needs (lattice_osr_ssm_saved_bytes(desc) bytes, 4-byte
+ * aligned: the states before every 16th token).  workspace must hold
+ * lattice_osr_ssm_workspace_bytes(desc) bytes, 16-byte aligned (NULL allowed
+ * where that is 0); its contents on entry are ignored, and calls that may
+ * overlap in time need one each.  Reruns agree bit for bit.
+ */
+LATTICE_OSR_API int lattice_osr_ssm_fwd(const lattice_osr_ssm_desc* desc, const void* x, const void* dt,
+                                        const float* A, const void* Bm, const void* Cm, const float* skip,
+                                        const void* z, const float* dt_bias, const int32_t* lengths,
+                                        const int32_t* segments, const float* state_in, float* state_out, void* y,
+                                        void* saved, size_t saved_bytes, void* workspace, size_t workspace_bytes,
+                                        void* hip_stream);
+
+/*
+ * Backward: the gradient of L = sum(dy * y) + sum(dstate_out * state_out),
+ * with the forward's inputs, descriptor and `saved` (unchanged since).
+ *   dy  [B, T, D] y_dtype;  dstate_out [B, D, N] float32, or NULL (zeros)
+ *   dx, ddt, dz  [B, T, D], dB, dC [B, T, G, N]  grad_dtype, contiguous, written in full
+ *                (zeros at padding); dz exactly where z is
+ *   dA [D, N], dskip [D], ddt_bias [D]  float32; dskip, ddt_bias only where skip,
+ *                dt_bias are; each NULL where it is not wanted
+ *   dstate_in  [B, D, N] float32, or NULL (not wanted)
+ * workspace: lattice_osr_ssm_bwd_workspace_bytes(desc) bytes, as the forward's.
+ */
+LATTICE_OSR_API int lattice_osr_ssm_bwd(const lattice_osr_ssm_desc* desc, const void* x, const void* dt,
+                                        const float* A, const void* Bm, const void* Cm, const float* skip,
+                                        const void* z, const float* dt_bias, const int32_t* lengths,
+                                        const int32_t* segments, const void* saved, size_t saved_bytes,
+                                        const void* dy, const float* dstate_out, void* dx, void* ddt, float* dA,
+                                        void* dB, void* dC, float* dskip, void* dz, float* ddt_bias, float* dstate_in,
+                                        void* workspace, size_t workspace_bytes, void* hip_stream);
+
+/* One token for each of B sequences (desc->T must be 1).  state_out may be state_in (in place).  No workspace. */
+LATTICE_OSR_API int lattice_osr_ssm_step(const lattice_osr_ssm_desc* desc, const void* x, const void* dt,
+                                         const float* A, const void* Bm, const void* Cm, const float* skip,
+                                         const void* z, const float* dt_bias, const float* state_in, float* state_out,
+                                         void* y, void* hip_stream);
+
+/* Bytes of `saved` and of the workspaces; (size_t)-1 for an invalid descriptor. */
+LATTICE_OSR_API size_t lattice_osr_ssm_saved_bytes(const lattice_osr_ssm_desc* desc);
+LATTICE_OSR_API size_t lattice_osr_ssm_workspace_bytes(const lattice_osr_ssm_desc* desc);
+LATTICE_OSR_API size_t lattice_osr_ssm_bwd_workspace_bytes(const lattice_osr_ssm_desc* desc);
+
+/*
+ * Layer norm with the residual in front of it: over rows of D values,
+ *   x' = x + y   (y NULL: x' = x),
+ *   z = (x' - mean(x')) / sqrt(var(x') + eps) w + b,   var the mean square of x' - mean(x').
+ * A w that is NULL is 1 throughout, a b that is NULL 0.  z is taken from x' in
+ * fp32, before x_out is rounded to its type; the variance from the differences, not from squares of x'.
+ *   y, z       [R, D]  in_dtype
+ *   x, x_out   [R, D]  res_dtype
+ *   w, b       [D]     float32
+ * D is at most 16384; alignment, eps and sums as for the norms above.
+ */
+typedef struct {
+    int32_t R;          /* rows                          */
+    int32_t D;          /* values per row                */
+    int32_t in_dtype;   /* of y, z and dz                */
+    int32_t res_dtype;  /* of x, x_out, dx_out and dx    */
+    int32_t grad_dtype; /* of dy                         */
+    float eps;
+} lattice_osr_layernorm_desc;
+
+/* Forward.  x_out may be NULL (not wanted; it must be without y) and may be x itself.  No other overlap of an output. */
+LATTICE_OSR_API int lattice_osr_layernorm_fwd(const lattice_osr_layernorm_desc* desc, const void* x, const void* y,
+                                              const float* w, const float* b, void* x_out, void* z, void* hip_stream);
+
+/*
+ * Backward: the gradient of L = sum(dx_out * x') + sum(dz * z), with the
+ * forward's inputs (which must not have been updated in place).
+ *   dx_out  [R, D] res_dtype, or NULL (zeros);  dz [R, D] in_dtype
+ *   dx      [R, D] res_dtype, may be dx_out itself;  dy [R, D] grad_dtype, only with y: the
+ *           same gradient in two types, one of them NULL where the other serves
+ *   dw, db  [D] float32, each NULL where it is not wanted
+ * workspace: lattice_osr_layernorm_bwd_workspace_bytes(desc) bytes, 4-byte aligned (NULL
+ * allowed without dw and db).  The sums over rows have a fixed order.
+ */
+LATTICE_OSR_API int lattice_osr_layernorm_bwd(const lattice_osr_layernorm_desc* desc, const void* x, const void* y,
+                                              const float* w, const void* dx_out, const void* dz, void* dx, void* dy,
+                                              float* dw, float* db, void* workspace, size_t workspace_bytes,
+                                              void* hip_stream);
+LATTICE_OSR_API size_t lattice_osr_layernorm_bwd_workspace_bytes(const lattice_osr_layernorm_desc* desc);
+
 /* Static text for a status code (never NULL). */
 LATTICE_OSR_API const char* lattice_osr_status_string(int status);
 

@@ -1,0 +1,482 @@
+"""GPU parity of the selective state space scan (lattice_osr_ssm_*) against the
+fp64 oracle (oracle/mixer.py), element by element.
+
+Bars: the oracle's own bounds (every fp32 rounding counted at the magnitude of
+its operands), plus half a step of a bf16 output (2^-8 of the value).
+"""
+import math
+
+import pytest
+import torch
+
+from compressed_memory_linear_amd import osr
+from oracle import mixer
+
+pytestmark = pytest.mark.gpu
+
+BF, F = torch.bfloat16, torch.float32
+
+
+def make(B, T, D, N, G=1, dtype=BF, seed=0, gate=True, skip=True, bias=True, state=True, step=0.05):
+    """Steps around `step`, decays -1 .. -N: memories from one token to some hundreds."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    raw = math.log(math.expm1(step))
+    x = dict(x=r(B, T, D).to(dtype), dt=(r(B, T, D) + (0.0 if bias else raw)).to(dtype),
+             A=-torch.arange(1, N + 1, device="cuda").float() * torch.exp(0.3 * r(D, N)),
+             B=r(B, T, G, N).to(dtype), C=r(B, T, G, N).to(dtype), state_in=r(B, D, N) if state else None,
+             D=r(D) if skip else None, z=r(B, T, D).to(dtype) if gate else None,
+             dt_bias=0.2 * r(D) + raw if bias else None)
+    return x
+
+
+def incoming(B, T, D, N, y_dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(1000 + seed)
+    return (torch.randn((B, T, D), generator=g, device="cuda").to(y_dtype),
+            torch.randn((B, D, N), generator=g, device="cuda"))
+
+
+def check(name, got, ref, bound):
+    ref, bound = ref.reshape(got.shape), bound.reshape(got.shape)
+    err = (got.double() - ref).abs()
+    lim = mixer.rounded(bound, ref, got.dtype)
+    assert torch.isfinite(got).all(), name
+    worst = float((err / lim).max()) if err.numel() else 0.0
+    print(f"  {name}: worst error / bar {worst:.3f}", flush=True)
+    assert worst <= 1.0, (name, worst)
+
+
+def oracle(x, dy=None, dso=None, **kw):
+    return mixer.ssm(x["x"], x["dt"], x["A"], x["B"], x["C"], x["state_in"], x["D"], x["z"], x["dt_bias"], dy=dy,
+                     dstate_out=dso, **kw)
+
+
+def forward(x, **kw):
+    return osr.lattice_osr_ssm_fwd(x["x"], x["dt"], x["A"], x["B"], x["C"], x["state_in"], D=x["D"], z=x["z"],
+                                   dt_bias=x["dt_bias"], **kw)
+
+
+def backward(x, dy, dso, saved, **kw):
+    return osr.lattice_osr_ssm_bwd(x["x"], x["dt"], x["A"], x["B"], x["C"], dy, dso, saved=saved, D=x["D"], z=x["z"],
+                                   dt_bias=x["dt_bias"], **kw)
+
+
+def run_all(x, y_dtype=F, grad_dtype=F, seed=0, **kw):
+    B, T, D = x["x"].shape
+    N = x["A"].shape[1]
+    print(f"ssm B{B} T{T} D{D} N{N} G{x['B'].shape[2]} {x['x'].dtype} y {y_dtype} grad {grad_dtype} "
+          f"{ {k: v is not None for k, v in kw.items()} }", flush=True)
+    dy, dso = incoming(B, T, D, N, y_dtype, seed)
+    y, st, saved = forward(x, y_dtype=y_dtype, save=True, **kw)
+    y2, st2 = forward(x, y_dtype=y_dtype, **kw)
+    g = backward(x, dy, dso, saved, grad_dtype=grad_dtype, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(st, st2)
+    out, bound = oracle(x, dy, dso, **kw)
+    got = dict(g, y=y, state_out=st)
+    assert set(got) == set(out)
+    for n in got:
+        check(n, got[n], out[n], bound[n])
+    return got
+
+
+SHAPES = [(1, 1, 1, 1, 1), (2, 3, 5, 2, 1), (1, 16, 64, 4, 1), (3, 17, 64, 16, 1), (2, 32, 66, 16, 2), (2, 33, 130, 13, 1),
+          (1, 500, 96, 16, 3), (5, 64, 128, 8, 1), (1, 1030, 64, 16, 1), (40, 9, 24, 16, 1), (2, 48, 70, 5, 1),
+          (1, 90, 130, 24, 1), (1, 90, 130, 32, 2), (1, 70, 68, 33, 1), (1, 100, 64, 64, 1), (2, 31, 40, 64, 2)]
+
+
+@pytest.mark.parametrize("B,T,D,N,G", SHAPES)
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_shapes(B, T, D, N, G, dtype):
+    run_all(make(B, T, D, N, G, dtype, seed=T), y_dtype=dtype, grad_dtype=dtype)
+
+
+@pytest.mark.parametrize("gate", [True, False])
+@pytest.mark.parametrize("skip,bias,state", [(True, True, False), (False, False, True), (False, True, True)])
+def test_operands_that_may_be_left_out(gate, skip, bias, state):
+    run_all(make(2, 70, 80, 16, dtype=F, seed=3, gate=gate, skip=skip, bias=bias, state=state))
+
+
+@pytest.mark.parametrize("dtype,y_dtype,grad_dtype", [(BF, F, BF), (BF, BF, F), (F, BF, BF), (F, F, BF), (F, BF, F)])
+def test_types(dtype, y_dtype, grad_dtype):
+    run_all(make(2, 50, 70, 16, dtype=dtype, seed=4), y_dtype=y_dtype, grad_dtype=grad_dtype)
+
+
+@pytest.mark.parametrize("step", [1e-4, 1e-3, 1.0, 5.0])
+def test_slow_and_fast_decays(step):
+    """From steps whose softplus is far below 1 (long memories) to decays that leave nothing of a state."""
+    run_all(make(1, 300, 64, 16, dtype=F, seed=5, step=step))
+
+
+def test_steps_as_they_are():
+    """softplus off: delta is dt itself, zeros (which keep the state) among them."""
+    x = make(2, 90, 70, 16, dtype=F, seed=6, bias=False)
+    x["dt"] = x["dt"].abs() * 0.02
+    x["dt"][:, 5:40] = 0
+    run_all(x, softplus=False)
+
+
+@pytest.mark.parametrize("D,N", [(64, 16), (65, 7), (66, 40)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_padded_batch(D, N, dtype):
+    """Lengths 0, 1, T, inside, at and next to the borders of tiles, and out of range; padding holds NaN,
+    infinities and the types' lowest values and reaches nothing."""
+    T = 150
+    lens = [0, 1, T, 15, 16, 17, 32, 33, 127, 128, 129, -5, T + 50]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    x = make(len(lens), T, D, N, dtype=dtype, seed=13)
+    dy, dso = incoming(len(lens), T, D, N, dtype)
+    bad = [math.nan, math.inf, -math.inf, torch.finfo(dtype).min]
+    clean = {k: None if t is None else t.clone() for k, t in x.items()}
+    dyc = dy.clone()
+    for i, k in enumerate(lens):
+        k = max(0, min(T, k))
+        for j, name in enumerate(("x", "dt", "B", "C", "z")):
+            x[name][i, k:] = bad[(i + j) % 4]
+            clean[name][i, k:] = 0
+        dy[i, k:] = bad[i % 4]
+        dyc[i, k:] = 0
+    y, st, saved = forward(x, y_dtype=dtype, save=True, lengths=n)
+    g = backward(x, dy, dso, saved, grad_dtype=dtype, lengths=n)
+    out, bound = oracle(clean, dyc, dso, lengths=n)
+    got = dict(g, y=y, state_out=st)
+    for name in got:
+        check(name, got[name], out[name], bound[name])
+    for i, k in enumerate(lens):
+        k = max(0, min(T, k))
+        for name in ("y", "dx", "ddt", "dz", "dB", "dC"):
+            assert (got[name][i, k:] == 0).all(), (name, i)
+        if k == 0:
+            assert torch.equal(st[i], x["state_in"][i]) and torch.equal(g["dstate_in"][i], dso[i])
+
+
+def test_all_sequences_empty():
+    x = make(3, 40, 50, 16)
+    got = run_all(x, lengths=torch.zeros(3, dtype=torch.int32, device="cuda"))
+    assert (got["y"] == 0).all() and torch.equal(got["state_out"], x["state_in"]) and (got["dA"] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_documents_packed_in_a_row(dtype):
+    """A border drops the state, whatever it was; the row equals its documents one by one.  Borders at, before and
+    behind those of tiles, one token apart, in padding, and numbers that come again."""
+    T = 140
+    x = make(2, T, 66, 16, dtype=dtype, seed=17)
+    cuts = [0, 15, 16, 17, 32, 64, 65, 66, 100, 128]
+    seg = torch.zeros((2, T), dtype=torch.int32, device="cuda")
+    for i, c in enumerate(cuts):
+        seg[:, c:] = [7, 3, 7, -1, 2 ** 31 - 1][i % 5]
+    n = torch.tensor([T, 120], dtype=torch.int32, device="cuda")
+    x["state_in"][0] = 1e30
+    got = run_all(x, segments=seg, lengths=n, y_dtype=F)
+    # the state drops out exactly: another one in front of the first border changes nothing behind it
+    other = dict(x, state_in=-x["state_in"])
+    y, st = forward(other, segments=seg, lengths=n)
+    assert torch.equal(y[:, 15:], got["y"][:, 15:]) and torch.equal(st, got["state_out"])
+    for a, b in zip(cuts, cuts[1:] + [T]):
+        if b > 120:
+            continue
+        part = {k: t[:, a:b].contiguous() if t is not None and k in ("x", "dt", "B", "C", "z") else t for k, t in x.items()}
+        part["state_in"] = x["state_in"] if a == 0 else None
+        out, bound = oracle(part)
+        check(f"document {a}", forward(part)[0], out["y"], bound["y"])
+        check(f"document {a} in the row", got["y"][:, a:b], out["y"], bound["y"])
+
+
+def test_a_border_drops_what_is_not_finite():
+    x = make(2, 100, 64, 16, dtype=F, seed=18)
+    seg = (torch.arange(100, device="cuda") >= 50).int().expand(2, 100).contiguous()
+    want = forward(x, segments=seg)
+    bad = dict(x, state_in=x["state_in"].clone(), x=x["x"].clone())
+    bad["state_in"][0] = math.inf
+    bad["x"][1, 20] = math.nan
+    y, st, sv = forward(bad, segments=seg, save=True)
+    assert torch.equal(y[:, 50:], want[0][:, 50:]) and torch.equal(st, want[1])
+    dy, dso = incoming(2, 100, 64, 16, F)
+    g0 = backward(bad, dy, dso, sv, segments=seg)
+    dso[0] = math.inf
+    dy[1, 70] = math.nan
+    g = backward(bad, dy, dso, sv, segments=seg)
+    for n in ("dx", "ddt", "dz", "dB", "dC"):
+        ok = torch.isfinite(g0[n][:, :50])
+        assert torch.equal(g[n][:, :50][ok], g0[n][:, :50][ok]), n
+
+
+def test_nan_stays_in_its_channel_and_behind():
+    x = make(2, 200, 64, 16, dtype=F, seed=19)
+    x["x"][0, 150, 7] = math.nan
+    x["dt"][1, 20, 9] = math.nan
+    y, st = forward(x)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[0, 150:, 7] = True
+    bad[1, 20:, 9] = True
+    assert torch.equal(torch.isnan(y), bad)
+    assert torch.equal(torch.isnan(st).all(-1), bad[:, -1]) and torch.equal(torch.isnan(st).any(-1), bad[:, -1])
+
+
+def shifted(t, off):
+    """t in an allocation of its own, `off` elements into it, NaN around."""
+    flat = torch.full((t.numel() + 16,), math.nan, dtype=t.dtype, device="cuda")
+    view = flat[off:off + t.numel()].view(t.shape)
+    view.copy_(t)
+    return flat, view
+
+
+@pytest.mark.parametrize("off", [1, 3])
+@pytest.mark.parametrize("N", [16, 6])
+def test_unaligned_buffers(off, N):
+    """Every buffer of the calls `off` elements into an allocation, and nothing written outside them."""
+    B, T, D = 2, 50, 64
+    x = make(B, T, D, N, seed=23)
+    s = {k: shifted(t, off)[1] for k, t in x.items()}
+    ref = forward(x, y_dtype=BF, save=True)
+    (yf, y), (sf, so) = shifted(torch.zeros_like(ref[0]), off), shifted(torch.zeros_like(ref[1]), off)
+    _, _, saved = forward(s, y_dtype=BF, y=y, state_out=so, save=True)
+    assert torch.equal(y, ref[0]) and torch.equal(so, ref[1])
+    dy, dso = incoming(B, T, D, N, BF)
+    g0 = backward(x, dy, dso, ref[2], grad_dtype=BF)
+    bufs = {k: shifted(torch.zeros_like(t), off) for k, t in g0.items()}
+    backward(s, shifted(dy, off)[1], shifted(dso, off)[1], saved, grad_dtype=BF, grads={k: v for k, (_, v) in bufs.items()})
+    for k, (flat, v) in dict(bufs, y=(yf, y), state=(sf, so)).items():
+        if k in g0:
+            assert torch.equal(v, g0[k]), k
+        assert torch.isnan(flat[:off]).all() and torch.isnan(flat[off + v.numel():]).all(), k
+    one = {k: t[:, :1].contiguous() if t.dim() >= 3 and k not in ("state_in", "A") else t for k, t in x.items()}
+    sh = {k: shifted(t, off)[1] for k, t in one.items()}
+    a = step(one, y_dtype=BF)
+    b = step(sh, y_dtype=BF, y=shifted(a[0], off)[1], state_out=shifted(a[1], off)[1])
+    assert torch.equal(a[0], b[0])
+    check("state", b[1], a[1].double(), a[1].double().abs() * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_rows_a_stride_apart(dtype):
+    """x, dt, z as parts of one projection's output and B, C as parts of another's, as a layer has them: the same as
+    their copies, forward, backward and step; what lies between the rows is not read into them."""
+    B, T, D, N, G = 2, 45, 66, 5, 2
+    x = make(B, T, D, N, G, dtype=dtype, seed=25)
+    wide = torch.full((B, T, 3 * D + 5), math.nan, dtype=dtype, device="cuda")
+    proj = torch.full((B, T, 2 * G * N + 7), math.nan, dtype=dtype, device="cuda")
+    v = dict(x)
+    for i, k in enumerate(("x", "dt", "z")):
+        v[k] = wide[..., i * D:(i + 1) * D]
+        v[k].copy_(x[k])
+    for i, k in enumerate(("B", "C")):
+        v[k] = proj[..., 3 + i * G * N:3 + (i + 1) * G * N].unflatten(-1, (G, N))
+        v[k].copy_(x[k])
+    dy, dso = incoming(B, T, D, N, F)
+    n = torch.tensor([T, 20], dtype=torch.int32, device="cuda")
+    res = []
+    for a in (x, v):
+        y, st, sv = forward(a, save=True, lengths=n)
+        res.append(dict(backward(a, dy, dso, sv, lengths=n), y=y, st=st))
+    for k in res[0]:
+        assert torch.equal(res[0][k], res[1][k]), k
+    cut = lambda a: {k: t[:, 3:4] if k in ("x", "dt", "z", "B", "C") else t for k, t in a.items()}
+    want = step({k: t.contiguous() for k, t in cut(x).items()})
+    got = step(cut(v))
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+def step(x, **kw):
+    return osr.lattice_osr_ssm_step(x["x"], x["dt"], x["A"], x["B"], x["C"], x["state_in"], D=x["D"], z=x["z"],
+                                    dt_bias=x["dt_bias"], **kw)
+
+
+def test_heads_layout():
+    """[B,T,H,d] tensors with [H,d,N], [H,d] parameters, one head to a group; and B, C without a group dimension."""
+    B, T, H, d, N = 2, 40, 3, 32, 16
+    x = make(B, T, H * d, N, H, seed=29)
+    shape = dict(x=(B, T, H, d), dt=(B, T, H, d), z=(B, T, H, d), A=(H, d, N), D=(H, d), dt_bias=(H, d),
+                 state_in=(B, H, d, N), B=(B, T, H, N), C=(B, T, H, N))
+    four = {k: t.view(shape[k]) for k, t in x.items()}
+    dy, dso = incoming(B, T, H * d, N, F)
+    y, st, sv = forward(x, save=True)
+    g = backward(x, dy, dso, sv)
+    y4, st4, sv4 = forward(four, save=True)
+    g4 = backward(four, dy.view(B, T, H, d), dso.view(B, H, d, N), sv4)
+    assert y4.shape == (B, T, H, d) and st4.shape == (B, H, d, N)
+    assert torch.equal(y4.view_as(y), y) and torch.equal(st4.view_as(st), st)
+    for k in g:
+        assert torch.equal(g4[k].reshape(g[k].shape), g[k]), k
+    one = make(B, T, 64, N, seed=30)
+    flat = dict(one, B=one["B"][:, :, 0], C=one["C"][:, :, 0])
+    assert torch.equal(forward(one)[0], forward(flat)[0])
+
+
+def test_state_in_place_at_every_length():
+    for T in (1, 31, 200, 3000):
+        x = make(2, T, 70, 16, seed=T)
+        want = forward(x)
+        for _ in range(2):
+            st = x["state_in"].clone()
+            y, _ = forward(dict(x, state_in=st), state_out=st)
+            assert torch.equal(y, want[0]) and torch.equal(st, want[1]), T
+
+
+@pytest.mark.parametrize("cut", [1, 16, 40, 200])
+def test_split_sequence_continues(cut):
+    """Two calls chained through the state, and the second part token by token, stay within the bars of one call."""
+    x = make(2, 230, 66, 16, seed=31)
+    out, bound = oracle(x)
+    part = lambda a, b, st: dict({k: t[:, a:b].contiguous() if k in ("x", "dt", "z", "B", "C") else t
+                                  for k, t in x.items()}, state_in=st)
+    y1, st = forward(part(0, cut, x["state_in"]))
+    y2, st2 = forward(part(cut, 230, st))
+    check("two calls", torch.cat([y1, y2], 1), out["y"], bound["y"])
+    check("state", st2, out["state_out"], bound["state_out"])
+    ys, state = [], st.clone()
+    for t in range(cut, 230):
+        yt, state = step(part(t, t + 1, state), state_out=state)
+        ys.append(yt.clone())
+    check("steps", torch.cat([y1] + ys, 1), out["y"], bound["y"])
+    check("state after steps", state, out["state_out"], bound["state_out"])
+
+
+@pytest.mark.parametrize("B,D,N,G", [(1, 1, 1, 1), (1, 64, 16, 1), (3, 33, 5, 1), (100, 130, 16, 2), (5, 256, 64, 1),
+                                     (4, 96, 30, 1), (2, 40, 8, 4), (3, 50, 12, 1)])
+@pytest.mark.parametrize("dtype,y_dtype", [(BF, BF), (BF, F), (F, F)])
+def test_step(B, D, N, G, dtype, y_dtype):
+    for full in (True, False):
+        x = make(B, 1, D, N, G, dtype, seed=37, gate=full, skip=full, bias=full)
+        y, st = step(x, y_dtype=y_dtype)
+        out, bound = oracle(x)
+        check("y", y, out["y"], bound["y"])
+        check("state", st, out["state_out"], bound["state_out"])
+        inplace = x["state_in"].clone()
+        y2, _ = step(dict(x, state_in=inplace), y_dtype=y_dtype, state_out=inplace)
+        assert torch.equal(y2, y) and torch.equal(inplace, st)
+
+
+@pytest.mark.parametrize("B,T,D,N,G", [(1, 5000, 64, 16, 1), (1, 2500, 320, 16, 1), (2, 2100, 128, 32, 2),
+                                       (1, 1300, 130, 64, 1), (9, 600, 512, 16, 1)])
+def test_long_and_wide(B, T, D, N, G):
+    """Few channels over many tiles, and enough of them to fill the chip; ragged and packed."""
+    g = torch.Generator(device="cuda").manual_seed(41)
+    x = make(B, T, D, N, G, seed=41, step=0.01)
+    n = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+    n[0] = T
+    seg = (torch.rand((B, T), generator=g, device="cuda") < 3 / T).cumsum(1).int()
+    run_all(x, y_dtype=BF, grad_dtype=BF)
+    run_all(x, lengths=n, segments=seg)
+
+
+def test_reruns_agree_bit_for_bit():
+    x = make(2, 3000, 192, 16, seed=43)
+    dy, dso = incoming(2, 3000, 192, 16, BF)
+    first = None
+    for _ in range(4):
+        y, st, sv = forward(x, save=True)
+        got = [y, st, sv, *backward(x, dy, dso, sv).values()]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_workspace_contents_do_not_matter():
+    """Whatever the workspaces and `saved` hold on entry; nothing is written behind them."""
+    B, T, D, N = 2, 3000, 130, 16
+    x = make(B, T, D, N, seed=47, step=0.01)
+    dy, dso = incoming(B, T, D, N, BF)
+    desc = osr.make_ssm_desc(B, T, D, N, 1, osr.BF16, osr.BF16, osr.F32)
+    sizes = (osr.lattice_osr_ssm_saved_bytes(desc), osr.lattice_osr_ssm_workspace_bytes(desc),
+             osr.lattice_osr_ssm_bwd_workspace_bytes(desc))
+    first = None
+    for fill in (0, 255, 0x7f, None):
+        bufs = [torch.empty(n + 256, dtype=torch.uint8, device="cuda") for n in sizes]
+        for t in bufs:
+            t.random_(0, 256) if fill is None else t.fill_(fill)
+        tails = [t[n:].clone() for t, n in zip(bufs, sizes)]
+        sv, ws, wb = (t[:n] for t, n in zip(bufs, sizes))
+        y, st, _ = forward(x, y_dtype=BF, saved=sv, workspace=ws)
+        got = [y, st, *backward(x, dy, dso, sv, workspace=wb).values()]
+        first = first or got
+        assert all(torch.equal(a, b) for a, b in zip(first, got)), fill
+        assert all(torch.equal(t[n:], tail) for t, n, tail in zip(bufs, sizes, tails))
+
+
+def test_captured_calls_and_another_stream():
+    """Forward, backward and step captured into a graph and replayed on new inputs with eager work between, and on a
+    stream of their own beside the same calls on the current one."""
+    B, T, D, N = 2, 1500, 130, 16
+    x, x2 = make(B, T, D, N, seed=51), make(B, T, D, N, seed=52)
+    dy, dso = incoming(B, T, D, N, F)
+
+    def both(a):
+        y, st, sv = forward(a, save=True)
+        return [y, st, *backward(a, dy, dso, sv).values()]
+
+    want = [t.clone() for t in both(x)], [t.clone() for t in both(x2)]
+    static = {k: t.clone() for k, t in x.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(static)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(static)
+    for i in (0, 1, 0, 1):
+        for k, t in static.items():
+            t.copy_((x, x2)[i][k])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want[i])), i
+        both(x2)
+        torch.cuda.synchronize()
+    side.wait_stream(torch.cuda.current_stream())
+    y, st, sv = forward(x, save=True, stream=side)
+    g = backward(x, dy, dso, sv, stream=side)
+    here = both(x2)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(a, b) for a, b in zip([y, st, *g.values()], want[0]))
+    assert all(torch.equal(a, b) for a, b in zip(here, want[1]))
+
+
+def test_outputs_that_may_be_left_out():
+    """The C entries without state_out, dA, dskip, ddt_bias, dstate_in: the others are as with them."""
+    import ctypes
+    B, T, D, N = 2, 70, 66, 16
+    x = make(B, T, D, N, seed=53)
+    dy, dso = incoming(B, T, D, N, F)
+    y, st, sv = forward(x, save=True)
+    g = backward(x, dy, dso, sv)
+    lib, p = osr.load_library(), (lambda t: t.data_ptr())
+    desc = osr.make_ssm_desc(B, T, D, N, 1, osr.BF16, osr.F32, osr.F32)
+    s = torch.cuda.current_stream().cuda_stream
+    ws = torch.empty(osr.lattice_osr_ssm_workspace_bytes(desc) + 16, dtype=torch.uint8, device="cuda")
+    wb = torch.empty(osr.lattice_osr_ssm_bwd_workspace_bytes(desc), dtype=torch.uint8, device="cuda")
+    y2 = torch.full_like(y, math.nan)
+    ins = [p(x[k]) for k in ("x", "dt", "A", "B", "C", "D", "z", "dt_bias")] + [None, None]
+    assert lib.lattice_osr_ssm_fwd(ctypes.byref(desc), *ins, p(x["state_in"]), None, p(y2), None, 0, p(ws), ws.numel(), s) == 0
+    assert torch.equal(y, y2)
+    o = {k: torch.full_like(g[k], math.nan) for k in ("dx", "ddt", "dB", "dC", "dz")}
+    assert lib.lattice_osr_ssm_bwd(ctypes.byref(desc), *ins, p(sv), sv.numel(), p(dy), p(dso), p(o["dx"]), p(o["ddt"]), None,
+                                   p(o["dB"]), p(o["dC"]), None, p(o["dz"]), None, None, p(wb), wb.numel(), s) == 0
+    for k in o:
+        assert torch.equal(o[k], g[k]), k
+
+
+def test_gradient_by_differences():
+    """Central differences of the fp32 forward's loss, summed in 64 bits, along random directions.  The loss is a sum of
+    B T D + B D N products of about unit size; a relative step of 2^-6 leaves a third-order term and rounding
+    below 2 % of the slope here (both measured on the oracle: see the assertion on it)."""
+    x = make(1, 40, 32, 8, dtype=F, seed=57)
+    dy, dso = incoming(1, 40, 32, 8, F)
+    y, st, sv = forward(x, save=True)
+    g = backward(x, dy, dso, sv)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+
+    def loss(fn, a):
+        yy, ss = fn(a)
+        return float((yy.double() * dy.double()).sum() + (ss.double() * dso.double()).sum())
+
+    ref = lambda a: (lambda o: (o["y"], o["state_out"]))(oracle(a)[0])
+    names = dict(x="dx", dt="ddt", A="dA", B="dB", C="dC", D="dD", z="dz", dt_bias="ddt_bias", state_in="dstate_in")
+    for k, n in names.items():
+        d = torch.randn(x[k].shape, generator=gen, device="cuda") * 2.0 ** -6
+        up, down = dict(x, **{k: x[k] + d}), dict(x, **{k: x[k] - d})
+        slope = float((g[n].double() * d.double()).sum()) * 2
+        scale = float((g[n].double() * d.double()).norm()) * 2
+        exact = loss(ref, up) - loss(ref, down)
+        assert abs(exact - slope) <= 0.02 * max(abs(slope), scale), n
+        assert abs(loss(lambda a: forward(a), up) - loss(lambda a: forward(a), down) - slope) <= 0.025 * max(abs(slope), scale), n
