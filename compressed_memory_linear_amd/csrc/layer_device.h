@@ -87,12 +87,12 @@ constexpr int kNt = 2;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const void* p, int64_t first, int bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(static_cast<char*>(const_cast<void*>(p)) + first, 0, bytes, 0x00020000);
 }
-template <typename T>
+template <typename T, bool NT = true>
 __device__ __forceinline__ T load_row(__amdgpu_buffer_rsrc_t r, uint32_t off) {
     if constexpr (sizeof(T) == 2)
-        return __builtin_bit_cast(T, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, kNt)));
+        return __builtin_bit_cast(T, static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, NT ? kNt : 0)));
     else
-        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, kNt));
+        return __builtin_bit_cast(T, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, NT ? kNt : 0));
 }
 // NT: written past the caches.
 template <bool BF16, bool NT>

@@ -7,18 +7,22 @@
 // and channel (delta, u, the gate) through LDS and each sums its own states' part of y.
 #pragma once
 
+#include <utility>
+
 #include "layer_device.h"
 #include "layer_launch.h"
 
 namespace layer {
 
+constexpr int kSsmTile = 32;  // tokens per tile of the forward
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // softplus(v) and its derivative.  With e = exp(-|v|) in [0, 1], softplus = max(v, 0) + log(1 + e) and
 // log(1 + e) = 2 atanh(t), t = e / (2 + e) <= 1/3: an odd polynomial of degree 9, the nearest in relative
 // error (4e-9, fitted for this by reweighted least squares), so that small steps keep their relative accuracy.
+template <bool ACC>
 __device__ __forceinline__ void softplus_parts(float v, float& d, float& slope) {
-    const float e = exp_of<true>(-fabsf(v));
+    const float e = exp_of<ACC>(-fabsf(v));
     const float t = e * __builtin_amdgcn_rcpf(2.0f + e), q = t * t;
     float s = 0.281783342f;
     s = fmaf(s, q, 0.279606014f);
@@ -52,12 +56,12 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, int chain) {
     return at;
 }
 
-// Rows of a tensor [B,T,D] (row elements apart) from token t0 on, as a buffer.
+// Rows of a tensor [B,T,D] (row elements apart) from token t0 on, as a buffer that ends with the last of
+// `rows` (of no bytes where the tensor is absent); `width` elements of a row count.
 template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t ssm_rows(const void* p, int b, int T_, int t0, int rows, int row, int D) {
-    const int64_t first = (static_cast<int64_t>(b) * T_ + t0) * row;
-    const int bytes = p && rows > 0 ? ((rows - 1) * row + D) * static_cast<int>(sizeof(T)) : 0;
-    return rows_rsrc(p, first * static_cast<int64_t>(sizeof(T)), bytes);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ssm_rows(const void* p, int64_t token, int rows, int row, int width) {
+    const int bytes = p && rows > 0 ? ((rows - 1) * row + width) * static_cast<int>(sizeof(T)) : 0;
+    return rows_rsrc(p, token * row * static_cast<int64_t>(sizeof(T)), bytes);
 }
 
 // Which tokens of a tile of up to 64 begin a document (bit i: token t0 + i); the same in every lane.
@@ -72,20 +76,123 @@ __device__ __forceinline__ uint64_t ssm_cuts(const SsmParams& p, int b, int t0, 
     return __ballot(cut);
 }
 
-// B and C of a tile's tokens as floats [token][2][NP], zeros past N and at padding (so that
-// whatever stands there reaches nothing).
-template <typename TIn, int NP, int TILE, int NT>
-__device__ __forceinline__ void ssm_load_bc(const SsmParams& p, const SsmPlace& me, int t0, int n, float (*bc)[2 * NP]) {
-    const int64_t row = static_cast<int64_t>(me.b) * p.T + t0;
-    const TIn* Bm = static_cast<const TIn*>(p.Bm) + row * p.b_row + me.g * p.N;
-    const TIn* Cm = static_cast<const TIn*>(p.Cm) + row * p.c_row + me.g * p.N;
-    for (int i = threadIdx.x; i < TILE * 2 * NP; i += NT) {
-        const int t = i / (2 * NP), k = i % (2 * NP), s = k % NP;
-        float v = 0.0f;
-        if (t < n && s < p.N) v = widen(k < NP ? Bm[static_cast<int64_t>(t) * p.b_row + s] : Cm[static_cast<int64_t>(t) * p.c_row + s]);
-        bc[t][k] = v;
+// f(0), f(1) .. as compile-time constants.
+template <int... I, typename F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of(std::make_integer_sequence<int, N>(), f);
+}
+
+// B and C are the same for every channel of a group.  A register holds one state's values of 16 tokens, the same in
+// each row of 16 lanes, and the vector instruction that multiplies with one of them takes it from its lane by itself
+// (row_newbcast): no load, no register and no instruction per value.  (As scalar loads, prefetched 4 tokens ahead
+// from a packed copy, they kept a wave waiting for 60 % of its time.)
+template <int K>
+__device__ __forceinline__ float bcast(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x150 + K, 0xf, 0xf, true));
+}
+
+// Four neighbouring elements at byte offset off of a buffer: in one piece, or one by one, of which those from
+// `count` on are outside.
+template <typename T, bool VEC, bool NT>
+__device__ __forceinline__ Vec<T, 4> load_quad(__amdgpu_buffer_rsrc_t r, uint32_t off, int count) {
+    if constexpr (VEC && sizeof(T) == 2) {
+        return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, NT ? kNt : 0));
+    } else if constexpr (VEC) {
+        return __builtin_bit_cast(Vec<T, 4>, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT ? kNt : 0));
+    } else {
+        Vec<T, 4> v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v.e[e] = load_row<T, NT>(r, e < count ? off + e * static_cast<uint32_t>(sizeof(T)) : kOut);
+        return v;
     }
 }
+template <bool VEC, bool BF16, bool NT>
+__device__ __forceinline__ void store_quad(__amdgpu_buffer_rsrc_t r, uint32_t off, int count, const float (&x)[4]) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    if constexpr (VEC && BF16) {
+        u32x2 w;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            w[j] = osr::f32_to_bf16_bits(x[2 * j]) | static_cast<uint32_t>(osr::f32_to_bf16_bits(x[2 * j + 1])) << 16;
+        __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, NT ? kNt : 0);
+    } else if constexpr (VEC) {
+        u32x4 w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = __float_as_uint(x[j]);
+        __builtin_amdgcn_raw_buffer_store_b128(w, r, off, 0, NT ? kNt : 0);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store_row<BF16, NT>(r, e < count ? off + e * (BF16 ? 2u : 4u) : kOut, x[e]);
+    }
+}
+
+// The channels whose inputs and outputs a thread takes: four neighbours, of the tokens threadIdx.x / 16,
+// + NT / 16 and so on of each tile.
+struct SsmQuad {
+    int row, c, count;  // the first of those tokens; channels c .. c + count - 1
+};
+__device__ __forceinline__ SsmQuad ssm_quad(const SsmParams& p, const SsmPlace& me, int chain) {
+    SsmQuad q;
+    const int width = p.D / p.G, k = chain % ssm_blocks(p) * 64 + (threadIdx.x & 15) * 4;
+    q.row = threadIdx.x >> 4;
+    q.c = me.g * width + k;
+    q.count = min(max(width - k, 0), 4);
+    return q;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t quad_offset(const SsmQuad& q, int row, int stride) {
+    return q.count > 0 ? static_cast<uint32_t>(row * stride + q.c) * static_cast<uint32_t>(sizeof(T)) : kOut;
+}
+// A weight of four channels, zeros where it is absent.
+__device__ __forceinline__ void quad_weights(const float* w, const SsmQuad& q, float (&o)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = w && e < q.count ? w[q.c + e] : 0.0f;
+}
+
+// B's or C's registers of a tile of TILE tokens: reg[16-token part][state], lanes as tokens.
+template <typename T, int SN, int TILE, bool VEC>
+struct SsmRegs {
+    Vec<T, 4> raw[TILE / 16][SN / 4];
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int l, int n0, int N, int row) {
+#pragma unroll
+        for (int i = 0; i < TILE / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < SN / 4; ++k) {
+                const int n = n0 + 4 * k;
+                const uint32_t off = static_cast<uint32_t>((16 * i + (l & 15)) * row + n) * static_cast<uint32_t>(sizeof(T));
+                raw[i][k] = load_quad<T, VEC, false>(r, n < N ? off : kOut, N - n);
+            }
+    }
+    __device__ __forceinline__ void get(float (&o)[TILE / 16][SN]) const {
+#pragma unroll
+        for (int i = 0; i < TILE / 16; ++i)
+#pragma unroll
+            for (int n = 0; n < SN; ++n) o[i][n] = widen(raw[i][n / 4].e[n % 4]);
+    }
+};
+
+// Whether inputs and outputs can move in quads of elements: the quads lie within a group and every row of every
+// tensor is aligned to one (B and C to a quad of states).
+inline bool ssm_vec(const SsmParams& p) {
+    if (p.D / p.G % 4 != 0 || p.N % 4 != 0) return false;
+    for (int row : {p.x_row, p.dt_row, p.z_row, p.b_row, p.c_row})
+        if (row % 4 != 0) return false;
+    const uintptr_t in = p.in_bf16 ? 8 : 16, y = p.y_bf16 ? 8 : 16, g = p.grad_bf16 ? 8 : 16;
+    for (const void* q : {p.x, p.dt, p.z, p.Bm, p.Cm})
+        if (reinterpret_cast<uintptr_t>(q) % in != 0) return false;
+    for (const void* q : {static_cast<const void*>(p.y), p.dy})
+        if (reinterpret_cast<uintptr_t>(q) % y != 0) return false;
+    for (const void* q : {p.dx, p.ddt, p.dz})
+        if (reinterpret_cast<uintptr_t>(q) % g != 0) return false;
+    return true;
+}
+
+__host__ __device__ inline int ssm_padded(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
 
 // Calls f with the states per lane and waves of a workgroup for N states.
 template <typename F>

@@ -17,6 +17,21 @@ namespace {
 
 constexpr int kTile = kSsmSave;
 
+// B and C of a tile's tokens as floats [token][2][NP], zeros past N and at padding (so that
+// whatever stands there reaches nothing).
+template <typename TIn, int NP, int TILE, int NT>
+__device__ __forceinline__ void ssm_load_bc(const SsmParams& p, const SsmPlace& me, int t0, int n, float (*bc)[2 * NP]) {
+    const int64_t row = static_cast<int64_t>(me.b) * p.T + t0;
+    const TIn* Bm = static_cast<const TIn*>(p.Bm) + row * p.b_row + me.g * p.N;
+    const TIn* Cm = static_cast<const TIn*>(p.Cm) + row * p.c_row + me.g * p.N;
+    for (int i = threadIdx.x; i < TILE * 2 * NP; i += NT) {
+        const int t = i / (2 * NP), k = i % (2 * NP), s = k % NP;
+        float v = 0.0f;
+        if (t < n && s < p.N) v = widen(k < NP ? Bm[static_cast<int64_t>(t) * p.b_row + s] : Cm[static_cast<int64_t>(t) * p.c_row + s]);
+        bc[t][k] = v;
+    }
+}
+
 // The workspace: sums of B's and C's gradients [block][B T][G][2][N], then those over tokens
 // [B][N + 2][D] (dA, dskip, ddt_bias).
 struct BwdSpace {
@@ -63,10 +78,11 @@ __global__ __launch_bounds__(NW * 64) void layer_ssm_bwd_kernel(SsmParams p) {
     for (int tile = tiles - 1; tile >= 0; --tile) {
         const int t0 = tile * kTile;
         const int rows = min(kTile, p.T - t0), valid = min(max(me.len - t0, 0), rows);
-        const auto xr = ssm_rows<TIn>(p.x, me.b, p.T, t0, valid, p.x_row, p.D);
-        const auto dr = ssm_rows<TIn>(p.dt, me.b, p.T, t0, valid, p.dt_row, p.D);
-        const auto zr = ssm_rows<TIn>(p.z, me.b, p.T, t0, valid, p.z_row, p.D);
-        const auto gr = ssm_rows<TDy>(p.dy, me.b, p.T, t0, valid, p.D, p.D);
+        const int64_t token = static_cast<int64_t>(me.b) * p.T + t0;
+        const auto xr = ssm_rows<TIn>(p.x, token, valid, p.x_row, p.D);
+        const auto dr = ssm_rows<TIn>(p.dt, token, valid, p.dt_row, p.D);
+        const auto zr = ssm_rows<TIn>(p.z, token, valid, p.z_row, p.D);
+        const auto gr = ssm_rows<TDy>(p.dy, token, valid, p.D, p.D);
         float x[R], d[R], slope[R], z[R], dy[R], g[R];
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -79,12 +95,12 @@ __global__ __launch_bounds__(NW * 64) void layer_ssm_bwd_kernel(SsmParams p) {
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             slope[i] = 1.0f;
-            if (p.softplus) softplus_parts(d[i], d[i], slope[i]);
+            if (p.softplus) softplus_parts<kAccurate<TIn>>(d[i], d[i], slope[i]);
             if (r0 + i >= valid) d[i] = 0.0f;
             g[i] = dy[i];
             if (p.z) {
                 float s, r;
-                sigmoid2<true>(z[i], s, r);
+                sigmoid2<kAccurate<TIn>>(z[i], s, r);
                 g[i] *= z[i] * s;
             }
             in[r0 + i][l] = make_float4(d[i], d[i] * x[i], g[i], 0.0f);
@@ -167,7 +183,7 @@ __global__ __launch_bounds__(NW * 64) void layer_ssm_bwd_kernel(SsmParams p) {
             float dx = fmaf(du, d[i], skip * g[i]), ddt = fmaf(du, x[i], q) * slope[i], dz = 0.0f;
             if (p.z) {
                 float s, r;
-                sigmoid2<true>(z[i], s, r);
+                sigmoid2<kAccurate<TIn>>(z[i], s, r);
                 dz = dy[i] * y * (s * fmaf(z[i], r, 1.0f));
             }
             if (!on) dx = ddt = dz = 0.0f;

@@ -23,10 +23,17 @@ NONE, SILU = 0, 1
 E_SOFTPLUS = 16 * U
 
 
-def _silu(z):
-    """phi, phi' and their absolute errors (logits taken as fp32 ones: the exponent keeps its low part)."""
+def _exponent(v, bf16):
+    """What the exponential of v is off by beside the hardware's error: for bf16 inputs its exponent is one rounded
+    product with a rounded log2(e), 1.25 |v| u (as in oracle/layer.py); for fp32 ones it keeps what these lose."""
+    return 2 * U + 1.25 * U * v.abs().clamp(max=100.0) if bf16 else torch.zeros_like(v)
+
+
+def _silu(z, bf16=False):
+    """phi, phi' and their absolute errors."""
     s, r = torch.sigmoid(z), torch.sigmoid(-z)
-    return z * s, s * (1 + z * r), (E_SIG + 2 * U) * (z * s).abs(), (3 * E_SIG + 4 * U) * s * (1 + (z * r).abs())
+    es = E_SIG + _exponent(z, bf16)
+    return z * s, s * (1 + z * r), (es + 2 * U) * (z * s).abs(), (3 * es + 4 * U) * s * (1 + (z * r).abs())
 
 
 def _tokens(lengths, segments, B, T, device):
@@ -52,6 +59,7 @@ def ssm(x, dt, A, Bm, Cm, state_in=None, D=None, z=None, dt_bias=None, softplus=
     zero = torch.zeros((), dtype=f8, device=dev)
     ok, cut = _tokens(lengths, segments, nb, T, dev)
     on = lambda t: torch.where(ok.view(nb, T, *([1] * (t.dim() - 2))), t, zero)
+    bf16 = dt.dtype == torch.bfloat16
     x, A = on(x.double()), A.double()
     raw = on(dt.double())
     eraw = torch.zeros_like(raw)
@@ -61,8 +69,9 @@ def ssm(x, dt, A, Bm, Cm, state_in=None, D=None, z=None, dt_bias=None, softplus=
     if softplus:
         slope = torch.sigmoid(raw)
         delta = on(raw.clamp(min=0) + torch.log1p(torch.exp(-raw.abs())))
-        edelta = E_SOFTPLUS * delta + slope * eraw
-        eslope = slope * (E_SIG + torch.sigmoid(-raw) * eraw)
+        ee = _exponent(raw, bf16)
+        edelta = (E_SOFTPLUS + ee) * delta + slope * eraw
+        eslope = slope * (E_SIG + ee + torch.sigmoid(-raw) * eraw)
     else:
         slope, delta, edelta, eslope = torch.ones_like(raw), raw, eraw, torch.zeros_like(raw)
     u = delta * x
@@ -72,7 +81,7 @@ def ssm(x, dt, A, Bm, Cm, state_in=None, D=None, z=None, dt_bias=None, softplus=
     phi = dphi = torch.ones_like(x)
     ephi = edphi = torch.zeros_like(x)
     if z is not None:
-        phi, dphi, ephi, edphi = _silu(on(z.double()))
+        phi, dphi, ephi, edphi = _silu(on(z.double()), bf16)
 
     def decay(t):
         """exp(delta A) and its error: A log2 e and the product 2.3 u of the exponent, the steps' own error, those of
