@@ -14,7 +14,7 @@
 
 namespace layer {
 
-constexpr int kSsmTile = 32;  // tokens per tile of the forward
+constexpr int kSsmTile = 16;  // tokens per tile of the forward
 constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // softplus(v) and its derivative.  With e = exp(-|v|) in [0, 1], softplus = max(v, 0) + log(1 + e) and
@@ -56,13 +56,22 @@ __device__ __forceinline__ SsmPlace ssm_place(const SsmParams& p, int chain) {
     return at;
 }
 
-// Rows of a tensor [B,T,D] (row elements apart) from token t0 on, as a buffer that ends with the last of
-// `rows` (of no bytes where the tensor is absent); `width` elements of a row count.
-template <typename T>
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t ssm_rows(const void* p, int64_t token, int rows, int row, int width) {
-    const int bytes = p && rows > 0 ? ((rows - 1) * row + width) * static_cast<int>(sizeof(T)) : 0;
-    return rows_rsrc(p, token * row * static_cast<int64_t>(sizeof(T)), bytes);
-}
+// The rows of a tensor [B,T,D] (row elements apart) of one tile after the other, each as a buffer that ends with
+// the last row in use (of no bytes where the tensor is absent); `width` elements of a row count.
+struct SsmStream {
+    uintptr_t at;
+    uint32_t row_bytes, width_bytes;
+    __device__ __forceinline__ SsmStream(const void* p, int64_t token, int row, int width, int size) {
+        row_bytes = p ? row * size : 0;
+        width_bytes = p ? width * size : 0;
+        at = reinterpret_cast<uintptr_t>(p) + static_cast<uint64_t>(token) * row_bytes;
+    }
+    __device__ __forceinline__ void move(int rows) { at += static_cast<int64_t>(rows) * row_bytes; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(int count) const {
+        const uint32_t bytes = count > 0 ? (count - 1) * row_bytes + width_bytes : 0;
+        return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(at), 0, bytes, 0x00020000);
+    }
+};
 
 // Which tokens of a tile of up to 64 begin a document (bit i: token t0 + i); the same in every lane.
 __device__ __forceinline__ uint64_t ssm_cuts(const SsmParams& p, int b, int t0, int n, int l) {
@@ -131,23 +140,31 @@ __device__ __forceinline__ void store_quad(__amdgpu_buffer_rsrc_t r, uint32_t of
     }
 }
 
-// The channels whose inputs and outputs a thread takes: four neighbours, of the tokens threadIdx.x / 16,
-// + NT / 16 and so on of each tile.
+// The channels whose inputs and outputs a thread takes: four neighbours, of every few tokens of each tile.  id: its
+// number among the threads that do so.
 struct SsmQuad {
     int row, c, count;  // the first of those tokens; channels c .. c + count - 1
+    int at;             // c in its block of 64
 };
-__device__ __forceinline__ SsmQuad ssm_quad(const SsmParams& p, const SsmPlace& me, int chain) {
+__device__ __forceinline__ SsmQuad ssm_quad(const SsmParams& p, const SsmPlace& me, int chain, int id) {
     SsmQuad q;
-    const int width = p.D / p.G, k = chain % ssm_blocks(p) * 64 + (threadIdx.x & 15) * 4;
-    q.row = threadIdx.x >> 4;
+    const int width = p.D / p.G, k = chain % ssm_blocks(p) * 64 + (id & 15) * 4;
+    q.row = id >> 4;
+    q.at = (id & 15) * 4;
     q.c = me.g * width + k;
     q.count = min(max(width - k, 0), 4);
     return q;
 }
-template <typename T>
-__device__ __forceinline__ uint32_t quad_offset(const SsmQuad& q, int row, int stride) {
-    return q.count > 0 ? static_cast<uint32_t>(row * stride + q.c) * static_cast<uint32_t>(sizeof(T)) : kOut;
-}
+// Byte offsets of its quads in a tile's rows, every `step` tokens.
+template <int K>
+struct QuadOffsets {
+    uint32_t at[K];
+    __device__ __forceinline__ QuadOffsets(const SsmQuad& q, int stride, int step, int size) {
+#pragma unroll
+        for (int i = 0; i < K; ++i)
+            at[i] = here(q.count > 0 ? static_cast<uint32_t>((q.row + i * step) * stride + q.c) * size : kOut);
+    }
+};
 // A weight of four channels, zeros where it is absent.
 __device__ __forceinline__ void quad_weights(const float* w, const SsmQuad& q, float (&o)[4]) {
 #pragma unroll
@@ -158,15 +175,23 @@ __device__ __forceinline__ void quad_weights(const float* w, const SsmQuad& q, f
 template <typename T, int SN, int TILE, bool VEC>
 struct SsmRegs {
     Vec<T, 4> raw[TILE / 16][SN / 4];
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, int l, int n0, int N, int row) {
+    uint32_t at[TILE / 16][SN / 4];
+    int count;  // states from n0 on
+    __device__ __forceinline__ void place(int l, int n0, int N, int row) {
+        count = N - n0;
 #pragma unroll
         for (int i = 0; i < TILE / 16; ++i)
 #pragma unroll
-            for (int k = 0; k < SN / 4; ++k) {
-                const int n = n0 + 4 * k;
-                const uint32_t off = static_cast<uint32_t>((16 * i + (l & 15)) * row + n) * static_cast<uint32_t>(sizeof(T));
-                raw[i][k] = load_quad<T, VEC, false>(r, n < N ? off : kOut, N - n);
-            }
+            for (int k = 0; k < SN / 4; ++k)
+                at[i][k] = here(4 * k < count ? static_cast<uint32_t>((16 * i + (l & 15)) * row + n0 + 4 * k) *
+                                                    static_cast<uint32_t>(sizeof(T))
+                                              : kOut);
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r) {
+#pragma unroll
+        for (int i = 0; i < TILE / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < SN / 4; ++k) raw[i][k] = load_quad<T, VEC, false>(r, at[i][k], count - 4 * k);
     }
     __device__ __forceinline__ void get(float (&o)[TILE / 16][SN]) const {
 #pragma unroll

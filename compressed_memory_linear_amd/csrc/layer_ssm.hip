@@ -9,6 +9,7 @@ namespace layer {
 namespace {
 
 constexpr int kTile = kSsmTile;
+static_assert(kTile == 16 && kTile == kSsmSave, "a tile's B and C lie across 16 lanes, and a state is saved before each");
 constexpr int kMaxSegs = 64;
 #ifndef WANT
 #define WANT 256
@@ -43,23 +44,156 @@ __device__ __forceinline__ float* map_of(const FwdSpace& ws, int chain, int k) {
     return ws.maps + (static_cast<int64_t>(chain) * ws.segs + k) * (NP + 1) * 64;
 }
 
+// The first NW waves walk over the states of a tile while kHelpers<NW> more form the next tile's delta and u, and y of
+// the tile before from the waves' parts of it; they meet once a tile.
 // MAPS: the segments' maps alone.
+template <int NW>
+constexpr int kHelpers = NW < 2 ? 2 : NW > 4 ? 4 : NW;
+
 template <typename TIn, int SN, int NW, bool MAPS, bool VEC>
-__global__ __launch_bounds__(NW * 64) void layer_ssm_fwd_kernel(SsmParams p, FwdSpace ws) {
-    constexpr int NP = SN * NW;            // states, with those that stand for none
-    constexpr int NT = NW * 64;
-    constexpr int K = kTile * 16 / NT;     // quads of a tile that a thread takes
+__global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel(SsmParams p, FwdSpace ws) {
+    constexpr int NP = SN * NW;                     // states, with those that stand for none
+    constexpr int HT = kHelpers<NW> * 64;           // threads that take inputs and outputs
+    constexpr int K = kTile * 16 / HT;              // quads of a tile that each of them takes
     constexpr bool kAcc = kAccurate<TIn>;
-    __shared__ float du[kTile][2][64];     // delta and u
-    __shared__ float part[MAPS ? 1 : NW][MAPS ? 1 : kTile][64];  // a wave's part of y
+    constexpr int kIn = sizeof(TIn);
+    __shared__ float du[2][kTile][2][64];           // delta and u
+    __shared__ float part[MAPS ? 1 : 2][MAPS ? 1 : NW][MAPS ? 1 : kTile][64];  // a wave's part of y
     const int chains = p.B * p.G * ssm_blocks(p);
     const int chain = blockIdx.x % chains, seg = blockIdx.x / chains;
     const SsmPlace me = ssm_place(p, chain);
-    const SsmQuad mine = ssm_quad(p, me, chain);
+    const int t_begin = static_cast<int>(seg * ws.length);
+    const int t_end = static_cast<int>(min(t_begin + ws.length, static_cast<int64_t>(p.T)));
+    const int tiles = (t_end - t_begin + kTile - 1) / kTile;
+    const int64_t token = static_cast<int64_t>(me.b) * p.T + t_begin;
+    // tokens of tile i of the segment, and those that are no padding
+    auto rows_of = [&](int i) { return min(kTile, t_end - t_begin - i * kTile); };
+    auto valid_of = [&](int i) { return min(me.len - t_begin - i * kTile, rows_of(i)); };
+
+    if (me.wave >= NW) {
+        const SsmQuad mine = ssm_quad(p, me, chain, threadIdx.x - NW * 64);
+        float bias[4], skip[4];
+        quad_weights(p.dt_bias, mine, bias);
+        quad_weights(p.skip, mine, skip);
+        const int ey = p.y_bf16 ? 2 : 4;
+        SsmStream xs(p.x, token, p.x_row, p.D, kIn), ds(p.dt, token, p.dt_row, p.D, kIn), zs(p.z, token, p.z_row, p.D, kIn);
+        SsmStream ys(p.y, token, p.D, p.D, ey);
+        const QuadOffsets<K> xo(mine, p.x_row, HT / 16, kIn), dO(mine, p.dt_row, HT / 16, kIn), zo(mine, p.z_row, HT / 16, kIn);
+        const QuadOffsets<K> yo(mine, p.D, HT / 16, ey);
+        struct Raw {
+            Vec<TIn, 4> x[K], z[MAPS ? 1 : K];
+        } before, now, next;  // of the tile whose y is formed, the one the others walk over, the next
+        Vec<TIn, 4> nd[K];
+        double steps[4] = {};  // the sums of this thread's tokens' steps
+        auto fetch = [&](int i) {
+            const int valid = valid_of(i);
+            const auto xr = xs.rows(valid), dr = ds.rows(valid), zr = zs.rows(valid);
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                next.x[k] = load_quad<TIn, VEC, true>(xr, xo.at[k], mine.count);
+                nd[k] = load_quad<TIn, VEC, true>(dr, dO.at[k], mine.count);
+                if constexpr (!MAPS) next.z[k] = load_quad<TIn, VEC, true>(zr, zo.at[k], mine.count);
+            }
+            xs.move(kTile), ds.move(kTile), zs.move(kTile);
+        };
+        // delta and u of tile i, whose inputs are `next`
+        auto inputs = [&](int i) {
+            const int valid = valid_of(i);
+            float d[K][4];
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d[k][e] = widen(nd[k].e[e]) + bias[e];
+            if (p.softplus) {
+                float slope;
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) softplus_parts<kAcc>(d[k][e], d[k][e], slope);
+            }
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int row = mine.row + k * (HT / 16);
+                float4 dv, uv;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if (row >= valid) d[k][e] = 0.0f;
+                    (&dv.x)[e] = d[k][e];
+                    (&uv.x)[e] = d[k][e] * widen(next.x[k].e[e]);
+                    if constexpr (MAPS) steps[e] += d[k][e];
+                }
+                *reinterpret_cast<float4*>(&du[i & 1][row][0][mine.at]) = dv;
+                *reinterpret_cast<float4*>(&du[i & 1][row][1][mine.at]) = uv;
+            }
+        };
+        // y of tile i, whose inputs are `before`
+        auto outputs = [&](int i) {
+            float y[K][4];
+#pragma unroll
+            for (int k = 0; k < K; ++k) {
+                const int row = mine.row + k * (HT / 16);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[k][e] = skip[e] * widen(before.x[k].e[e]);
+#pragma unroll
+                for (int w = 0; w < NW; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(&part[i & 1][w][row][mine.at]);
+                    y[k][0] += v.x, y[k][1] += v.y, y[k][2] += v.z, y[k][3] += v.w;
+                }
+            }
+            if (p.z) {
+#pragma unroll
+                for (int k = 0; k < K; ++k)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float z = widen(before.z[k].e[e]);
+                        float s, r;
+                        sigmoid2<kAcc>(z, s, r);
+                        y[k][e] *= z * s;
+                    }
+            }
+            const int valid = valid_of(i);
+            const auto yr = ys.rows(rows_of(i));
+            ys.move(kTile);
+            with_flag(p.y_bf16, [&](auto bf16) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) {
+                    const int row = mine.row + k * (HT / 16);
+                    if (row >= valid) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
+                    store_quad<VEC, bf16(), false>(yr, yo.at[k], mine.count, y[k]);
+                }
+            });
+        };
+        fetch(0);
+        inputs(0);
+        now = next;
+        if (tiles > 1) fetch(1);
+        __syncthreads();
+        for (int i = 0; i < tiles; ++i) {
+            if constexpr (!MAPS) {
+                if (i > 0) outputs(i - 1);
+                before = now;
+            }
+            if (i + 1 < tiles) {
+                inputs(i + 1);
+                now = next;
+                if (i + 2 < tiles) fetch(i + 2);
+            }
+            __syncthreads();
+        }
+        if constexpr (MAPS) {
+            // the sum of the steps, by channel; the last tile's are done with
+            double* sums = reinterpret_cast<double*>(&du[0][0][0][0]);  // [HT / 16][64]
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[mine.row * 64 + mine.at + e] = steps[e];
+            __syncthreads();
+        } else {
+            outputs(tiles - 1);
+        }
+        return;
+    }
+
     const int wave = me.wave, l = me.l, c = me.c, n0 = wave * SN;
-    float A[SN], h[SN], bias[4], skip[4];
-    quad_weights(p.dt_bias, mine, bias);
-    quad_weights(p.skip, mine, skip);
+    float A[SN], h[SN];
     const int64_t state = (static_cast<int64_t>(me.b) * p.D + c) * p.N + n0;
 #pragma unroll
     for (int n = 0; n < SN; ++n) {
@@ -81,149 +215,78 @@ __global__ __launch_bounds__(NW * 64) void layer_ssm_fwd_kernel(SsmParams p, Fwd
             }
         }
     }
-    const int t_begin = static_cast<int>(seg * ws.length), t_end = static_cast<int>(min(t_begin + ws.length, static_cast<int64_t>(p.T)));
-    struct Raw {
-        Vec<TIn, 4> x[K], d[K], z[MAPS ? 1 : K];
-        SsmRegs<TIn, SN, kTile, VEC> b, c;
-    } next;
-    auto fetch = [&](int t0) {
-        const int valid = min(max(me.len - t0, 0), min(kTile, t_end - t0));
-        const int64_t token = static_cast<int64_t>(me.b) * p.T + t0;
-        const auto xr = ssm_rows<TIn>(p.x, token, valid, p.x_row, p.D);
-        const auto dr = ssm_rows<TIn>(p.dt, token, valid, p.dt_row, p.D);
-        const auto zr = ssm_rows<TIn>(p.z, token, MAPS ? 0 : valid, p.z_row, p.D);
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int row = mine.row + i * (NT / 16);
-            next.x[i] = load_quad<TIn, VEC, true>(xr, quad_offset<TIn>(mine, row, p.x_row), mine.count);
-            next.d[i] = load_quad<TIn, VEC, true>(dr, quad_offset<TIn>(mine, row, p.dt_row), mine.count);
-            if constexpr (!MAPS) next.z[i] = load_quad<TIn, VEC, true>(zr, quad_offset<TIn>(mine, row, p.z_row), mine.count);
-        }
-        const TIn *Bg = static_cast<const TIn*>(p.Bm) + me.g * p.N, *Cg = static_cast<const TIn*>(p.Cm) + me.g * p.N;
-        next.b.load(ssm_rows<TIn>(Bg, token, valid, p.b_row, p.N), l, n0, p.N, p.b_row);
-        if constexpr (!MAPS) next.c.load(ssm_rows<TIn>(Cg, token, valid, p.c_row, p.N), l, n0, p.N, p.c_row);
+    SsmRegs<TIn, SN, kTile, VEC> nb, nc;
+    nb.place(l, n0, p.N, p.b_row);
+    nc.place(l, n0, p.N, p.c_row);
+    SsmStream bs(static_cast<const TIn*>(p.Bm) + me.g * p.N, token, p.b_row, p.N, kIn);
+    SsmStream cs(static_cast<const TIn*>(p.Cm) + me.g * p.N, token, p.c_row, p.N, kIn);
+    auto fetch = [&](int i) {
+        const int valid = valid_of(i);
+        nb.load(bs.rows(valid));
+        if constexpr (!MAPS) nc.load(cs.rows(valid));
+        bs.move(kTile), cs.move(kTile);
     };
-    fetch(t_begin);
-    double steps[4] = {};  // the sums of this thread's tokens' steps
+    fetch(0);
     bool dropped = false;
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile) {
-        const int rows = min(kTile, t_end - t0), valid = min(max(me.len - t0, 0), rows);
-        float x[K][4], z[MAPS ? 1 : K][4], B[kTile / 16][SN], C[kTile / 16][SN];
-        next.b.get(B);
-        if constexpr (!MAPS) next.c.get(C);
-        float d[K][4];
-#pragma unroll
-        for (int i = 0; i < K; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                d[i][e] = widen(next.d[i].e[e]) + bias[e];
-                x[i][e] = widen(next.x[i].e[e]);
-                if constexpr (!MAPS) z[i][e] = widen(next.z[i].e[e]);
-            }
-        if (t0 + kTile < t_end) fetch(t0 + kTile);
-        if (p.softplus) {
-            float slope;
-#pragma unroll
-            for (int i = 0; i < K; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) softplus_parts<kAcc>(d[i][e], d[i][e], slope);
-        }
-#pragma unroll
-        for (int i = 0; i < K; ++i) {
-            const int row = mine.row + i * (NT / 16);
-            float4 dv, uv;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (row >= valid) d[i][e] = 0.0f;
-                (&dv.x)[e] = d[i][e];
-                (&uv.x)[e] = d[i][e] * x[i][e];
-                if constexpr (MAPS) steps[e] += d[i][e];
-            }
-            *reinterpret_cast<float4*>(&du[row][0][(threadIdx.x & 15) * 4]) = dv;
-            *reinterpret_cast<float4*>(&du[row][1][(threadIdx.x & 15) * 4]) = uv;
-        }
+    __syncthreads();
+    for (int i = 0; i < tiles; ++i) {
+        const int t0 = t_begin + i * kTile, valid = valid_of(i);
+        float B[1][SN], C[1][SN];
+        nb.get(B);
+        if constexpr (!MAPS) nc.get(C);
+        if (i + 1 < tiles) fetch(i + 1);
         const uint64_t cuts = ssm_cuts(p, me.b, t0, valid, l);
         dropped = dropped || cuts != 0;
-        __syncthreads();
+        if (!MAPS && p.saved && me.live) {
+            const int64_t of = tiles_of(p.T, kSsmSave);
+            float* to = p.saved + (me.b * of + t0 / kSsmSave) * p.N * p.D + c;
+#pragma unroll
+            for (int n = 0; n < SN; ++n)
+                if (n0 + n < p.N) to[static_cast<int64_t>(n0 + n) * p.D] = cuts & 1 ? 0.0f : h[n];
+        }
         with_flag(cuts != 0, [&](auto with_cuts) {
+            const float(*from)[2][64] = du[i & 1];
+            float dn[2][4], un[2][4];  // steps and inputs of four tokens, and of the next four
+#pragma unroll
+            for (int j = 0; j < 4; ++j) dn[0][j] = from[j][0][l], un[0][j] = from[j][1][l];
             each<kTile>([&](auto tc) {
                 constexpr int t = tc();
                 if (with_cuts() && (cuts >> t & 1)) {
 #pragma unroll
                     for (int n = 0; n < SN; ++n) h[n] = 0.0f;
                 }
-                if (!MAPS && t % kSsmSave == 0 && p.saved && t < rows && me.live) {
-                    const int64_t tiles = tiles_of(p.T, kSsmSave);
-                    float* to = p.saved + (me.b * tiles + (t0 + t) / kSsmSave) * p.N * p.D + c;
+                if constexpr (t % 4 == 0 && t + 4 < kTile) {
+                    constexpr int to = (t / 4 + 1) % 2;
 #pragma unroll
-                    for (int n = 0; n < SN; ++n)
-                        if (n0 + n < p.N) to[static_cast<int64_t>(n0 + n) * p.D] = h[n];
+                    for (int j = 0; j < 4; ++j) dn[to][j] = from[t + 4 + j][0][l], un[to][j] = from[t + 4 + j][1][l];
                 }
-                const float step = du[t][0][l], u = du[t][1][l];
+                const float step = dn[t / 4 % 2][t % 4], u = un[t / 4 % 2][t % 4];
                 float y[SN];
 #pragma unroll
                 for (int n = 0; n < SN; ++n) {
-                    h[n] = fmaf(__builtin_amdgcn_exp2f(step * A[n]), h[n], bcast<t % 16>(B[t / 16][n]) * u);
-                    if constexpr (!MAPS) y[n] = bcast<t % 16>(C[t / 16][n]) * h[n];
+                    h[n] = fmaf(__builtin_amdgcn_exp2f(step * A[n]), h[n], bcast<t>(B[0][n]) * u);
+                    if constexpr (!MAPS) y[n] = bcast<t>(C[0][n]) * h[n];
                 }
                 if constexpr (!MAPS) {
 #pragma unroll
                     for (int k = 1; k < SN; k *= 2)
 #pragma unroll
                         for (int n = 0; n < SN; n += 2 * k) y[n] += y[n + k];
-                    part[wave][t][l] = y[0];
+                    part[i & 1][wave][t][l] = y[0];
                 }
             });
         });
         __syncthreads();
-        if constexpr (!MAPS) {
-            const int size = p.y_bf16 ? 2 : 4;
-            const auto yr = rows_rsrc(p.y, (static_cast<int64_t>(me.b) * p.T + t0) * p.D * size, rows * p.D * size);
-            float y[K][4];
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-                const int row = mine.row + i * (NT / 16);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[i][e] = skip[e] * x[i][e];
-#pragma unroll
-                for (int w = 0; w < NW; ++w) {
-                    const float4 v = *reinterpret_cast<const float4*>(&part[w][row][(threadIdx.x & 15) * 4]);
-                    y[i][0] += v.x, y[i][1] += v.y, y[i][2] += v.z, y[i][3] += v.w;
-                }
-            }
-            if (p.z) {
-#pragma unroll
-                for (int i = 0; i < K; ++i)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float s, r;
-                        sigmoid2<kAcc>(z[i][e], s, r);
-                        y[i][e] *= z[i][e] * s;
-                    }
-            }
-            with_flag(p.y_bf16, [&](auto bf16) {
-#pragma unroll
-                for (int i = 0; i < K; ++i) {
-                    const int row = mine.row + i * (NT / 16);
-                    if (row >= valid) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0.0f;
-                    using T = std::conditional_t<bf16(), uint16_t, float>;
-                    store_quad<VEC, bf16(), false>(yr, quad_offset<T>(mine, row, p.D), mine.count, y[i]);
-                }
-            });
-        }
     }
     if constexpr (MAPS) {
         float* m = map_of<NP>(ws, chain, seg) + l;
 #pragma unroll
         for (int n = 0; n < SN; ++n) m[(n0 + n) * 64] = h[n];
-        // the sums of steps: 4 channels of NT / 16 threads each
-        double* sums = reinterpret_cast<double*>(&du[0][0][0]);  // [NT / 16][64]; the last tile's steps are done with
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sums[mine.row * 64 + (threadIdx.x & 15) * 4 + e] = steps[e];
         __syncthreads();
         if (wave == 0) {
+            const double* sums = reinterpret_cast<const double*>(&du[0][0][0][0]);
             double s = 0.0;
-            for (int i = 0; i < NT / 16; ++i) s += sums[i * 64 + l];
+            for (int j = 0; j < HT / 16; ++j) s += sums[j * 64 + l];
             m[NP * 64] = dropped ? __builtin_inff() : static_cast<float>(s);
         }
     } else if (p.state_out && me.live && seg == ws.segs - 1) {
@@ -295,7 +358,7 @@ void launch_fwd(const SsmParams& p, hipStream_t st) {
     with_states(p.N, [&](auto sn, auto nw) {
         const unsigned chains = static_cast<unsigned>(p.B) * p.G * tiles_of(p.D / p.G, 64);
         auto go = [&](auto vec) {
-            const dim3 block(nw() * 64);
+            const dim3 block((nw() + kHelpers<nw()>) * 64);
             if (ws.segs > 1)
                 hipLaunchKernelGGL((layer_ssm_fwd_kernel<TIn, sn(), nw(), true, vec()>), dim3(chains * (ws.segs - 1)), block,
                                    0, st, p, ws);

@@ -17,6 +17,12 @@ namespace {
 
 constexpr int kTile = kSsmSave;
 
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t ssm_rows(const void* p, int64_t token, int rows, int row, int width) {
+    const int bytes = p && rows > 0 ? ((rows - 1) * row + width) * static_cast<int>(sizeof(T)) : 0;
+    return rows_rsrc(p, token * row * static_cast<int64_t>(sizeof(T)), bytes);
+}
+
 // B and C of a tile's tokens as floats [token][2][NP], zeros past N and at padding (so that
 // whatever stands there reaches nothing).
 template <typename TIn, int NP, int TILE, int NT>
