@@ -98,7 +98,9 @@ __device__ __forceinline__ void each(F&& f) {
 // B and C are the same for every channel of a group.  A register holds one state's values of 16 tokens, the same in
 // each row of 16 lanes, and the vector instruction that multiplies with one of them takes it from its lane by itself
 // (row_newbcast): no load, no register and no instruction per value.  (As scalar loads, prefetched 4 tokens ahead
-// from a packed copy, they kept a wave waiting for 60 % of its time.)
+// from a packed copy, they kept a wave waiting for 60 % of its time.  The products are outer products of states and lanes,
+// which the matrix cores' sixteen blocks of 4 x 4 x 1 form in fp32, but one of those instructions takes the
+// vector unit 16 cycles beside other work, no less than the four that it stands for: B8 T4096 D2048 317 -> 373 us.)
 template <int K>
 __device__ __forceinline__ float bcast(float x) {
     return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), 0x150 + K, 0xf, 0xf, true));
@@ -171,33 +173,27 @@ __device__ __forceinline__ void quad_weights(const float* w, const SsmQuad& q, f
     for (int e = 0; e < 4; ++e) o[e] = w && e < q.count ? w[q.c + e] : 0.0f;
 }
 
-// B's or C's registers of a tile of TILE tokens: reg[16-token part][state], lanes as tokens.
-template <typename T, int SN, int TILE, bool VEC>
+// B or C of a tile's 16 tokens, a register per state: lanes as tokens, the same in each row of 16.
+template <typename T, int SN, bool VEC>
 struct SsmRegs {
-    Vec<T, 4> raw[TILE / 16][SN / 4];
-    uint32_t at[TILE / 16][SN / 4];
+    static constexpr int Q = SN / 4;
+    Vec<T, 4> raw[Q];
+    uint32_t at[Q];
     int count;  // states from n0 on
     __device__ __forceinline__ void place(int l, int n0, int N, int row) {
         count = N - n0;
 #pragma unroll
-        for (int i = 0; i < TILE / 16; ++i)
-#pragma unroll
-            for (int k = 0; k < SN / 4; ++k)
-                at[i][k] = here(4 * k < count ? static_cast<uint32_t>((16 * i + (l & 15)) * row + n0 + 4 * k) *
-                                                    static_cast<uint32_t>(sizeof(T))
-                                              : kOut);
+        for (int k = 0; k < Q; ++k)
+            at[k] = here(4 * k < count ? static_cast<uint32_t>((l & 15) * row + n0 + 4 * k) * static_cast<uint32_t>(sizeof(T))
+                                       : kOut);
     }
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r) {
 #pragma unroll
-        for (int i = 0; i < TILE / 16; ++i)
-#pragma unroll
-            for (int k = 0; k < SN / 4; ++k) raw[i][k] = load_quad<T, VEC, false>(r, at[i][k], count - 4 * k);
+        for (int k = 0; k < Q; ++k) raw[k] = load_quad<T, VEC, false>(r, at[k], count - 4 * k);
     }
-    __device__ __forceinline__ void get(float (&o)[TILE / 16][SN]) const {
+    __device__ __forceinline__ void get(float (&o)[SN]) const {
 #pragma unroll
-        for (int i = 0; i < TILE / 16; ++i)
-#pragma unroll
-            for (int n = 0; n < SN; ++n) o[i][n] = widen(raw[i][n / 4].e[n % 4]);
+        for (int n = 0; n < SN; ++n) o[n] = widen(raw[n / 4].e[n % 4]);
     }
 };
 
@@ -218,6 +214,28 @@ inline bool ssm_vec(const SsmParams& p) {
 }
 
 __host__ __device__ inline int ssm_padded(int N) { return N <= 4 ? 4 : N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+
+// The time axis in segments of whole tiles.  One of them where the chains' waves nearly fill the device's 1024 vector units,
+// since taking every segment twice costs two thirds more; else as many as make four waves for each, which hide one
+// another's waits.  Forward, D2048 N16 bf16: B8 T4096 (1024 waves) 1 segment 321 us, 3 411; B1 T65536 (128 waves) 8
+// segments 1051, 24 876, 32 867; B7 T1531 D1001 N13 padded fp32 (448 waves) 2 149, 6 130, 9 122.
+struct SsmSplit {
+    int64_t chains, length;
+    int segs;
+};
+inline SsmSplit ssm_split(const SsmParams& p) {
+    SsmSplit s;
+    s.chains = tiles_of(p.D / p.G, 64) * p.G * p.B;
+    const int64_t waves = s.chains * (p.N <= 4 ? 1 : p.N <= 8 ? 2 : p.N <= 16 ? 4 : 8), tiles = tiles_of(p.T, kSsmTile);
+    int64_t want = waves > 704 ? 1 : 4096 / waves;
+    if (want > 64) want = 64;
+    if (want > tiles / 4) want = tiles / 4;  // 64 tokens or more each
+    if (want < 1) want = 1;
+    const int per = static_cast<int>(tiles_of(tiles, static_cast<int>(want)));
+    s.length = static_cast<int64_t>(per) * kSsmTile;
+    s.segs = static_cast<int>(tiles_of(tiles, per));
+    return s;
+}
 
 // Calls f with the states per lane and waves of a workgroup for N states.
 template <typename F>

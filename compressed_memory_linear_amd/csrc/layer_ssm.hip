@@ -10,11 +10,6 @@ namespace {
 
 constexpr int kTile = kSsmTile;
 static_assert(kTile == 16 && kTile == kSsmSave, "a tile's B and C lie across 16 lanes, and a state is saved before each");
-constexpr int kMaxSegs = 64;
-#ifndef WANT
-#define WANT 256
-#endif
-
 // The workspace: the segments' maps [chain][segment][state, sum of steps][64].
 struct FwdSpace {
     float* maps;
@@ -22,19 +17,12 @@ struct FwdSpace {
     int64_t length;  // tokens per segment, whole tiles
     size_t bytes;
 };
-__host__ __device__ inline FwdSpace fwd_space(const SsmParams& p) {
+inline FwdSpace fwd_space(const SsmParams& p) {
     FwdSpace s;
-    const int64_t blocks = (p.D / p.G + 63) / 64, chains = blocks * p.G * p.B, tiles = tiles_of(p.T, kTile);
-    // workgroups of as many waves as a state has quads
-    int64_t want = WANT / chains;
-    want = want < 1 ? 1 : want > kMaxSegs ? kMaxSegs : want;
-    if (want > tiles / 4) want = tiles / 4;
-    if (want < 1) want = 1;
-    const int64_t per = tiles_of(tiles, static_cast<int>(want));
-    s.length = per * kTile;
-    s.segs = static_cast<int>(tiles_of(tiles, static_cast<int>(per)));
+    const SsmSplit k = ssm_split(p);
     s.maps = static_cast<float*>(p.ws);
-    s.bytes = s.segs > 1 ? static_cast<size_t>(chains) * s.segs * (ssm_padded(p.N) + 1) * 64 * sizeof(float) : 0;
+    s.segs = k.segs, s.length = k.length;
+    s.bytes = s.segs > 1 ? static_cast<size_t>(k.chains) * s.segs * (ssm_padded(p.N) + 1) * 64 * sizeof(float) : 0;
     return s;
 }
 
@@ -48,7 +36,7 @@ __device__ __forceinline__ float* map_of(const FwdSpace& ws, int chain, int k) {
 // the tile before from the waves' parts of it; they meet once a tile.
 // MAPS: the segments' maps alone.
 template <int NW>
-constexpr int kHelpers = NW < 2 ? 2 : NW > 4 ? 4 : NW;
+constexpr int kHelpers = NW < 4 ? 2 : 4;
 
 template <typename TIn, int SN, int NW, bool MAPS, bool VEC>
 __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel(SsmParams p, FwdSpace ws) {
@@ -81,29 +69,35 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
         const QuadOffsets<K> xo(mine, p.x_row, HT / 16, kIn), dO(mine, p.dt_row, HT / 16, kIn), zo(mine, p.z_row, HT / 16, kIn);
         const QuadOffsets<K> yo(mine, p.D, HT / 16, ey);
         struct Raw {
-            Vec<TIn, 4> x[K], z[MAPS ? 1 : K];
-        } before, now, next;  // of the tile whose y is formed, the one the others walk over, the next
-        Vec<TIn, 4> nd[K];
+            Vec<TIn, 4> x[K], z[MAPS ? 1 : K], d[K];
+        } raw[2];  // inputs on their way, of a tile with an even and one with an odd number
+        struct Kept {
+            Vec<TIn, 4> x[K], z[K];
+        } kept[2];  // what y takes of them
         double steps[4] = {};  // the sums of this thread's tokens' steps
-        auto fetch = [&](int i) {
+        auto fetch = [&](int i, auto odd) {
+            if (i >= tiles) return;
+            Raw& next = raw[odd()];
             const int valid = valid_of(i);
             const auto xr = xs.rows(valid), dr = ds.rows(valid), zr = zs.rows(valid);
 #pragma unroll
             for (int k = 0; k < K; ++k) {
                 next.x[k] = load_quad<TIn, VEC, true>(xr, xo.at[k], mine.count);
-                nd[k] = load_quad<TIn, VEC, true>(dr, dO.at[k], mine.count);
+                next.d[k] = load_quad<TIn, VEC, true>(dr, dO.at[k], mine.count);
                 if constexpr (!MAPS) next.z[k] = load_quad<TIn, VEC, true>(zr, zo.at[k], mine.count);
             }
             xs.move(kTile), ds.move(kTile), zs.move(kTile);
         };
-        // delta and u of tile i, whose inputs are `next`
-        auto inputs = [&](int i) {
+        // delta and u of tile i
+        auto inputs = [&](int i, auto odd) {
+            if (i >= tiles) return;
+            const Raw& next = raw[odd()];
             const int valid = valid_of(i);
             float d[K][4];
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d[k][e] = widen(nd[k].e[e]) + bias[e];
+                for (int e = 0; e < 4; ++e) d[k][e] = widen(next.d[k].e[e]) + bias[e];
             if (p.softplus) {
                 float slope;
 #pragma unroll
@@ -122,12 +116,14 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
                     (&uv.x)[e] = d[k][e] * widen(next.x[k].e[e]);
                     if constexpr (MAPS) steps[e] += d[k][e];
                 }
-                *reinterpret_cast<float4*>(&du[i & 1][row][0][mine.at]) = dv;
-                *reinterpret_cast<float4*>(&du[i & 1][row][1][mine.at]) = uv;
+                *reinterpret_cast<float4*>(&du[odd()][row][0][mine.at]) = dv;
+                *reinterpret_cast<float4*>(&du[odd()][row][1][mine.at]) = uv;
+                if constexpr (!MAPS) kept[odd()].x[k] = next.x[k], kept[odd()].z[k] = next.z[k];
             }
         };
-        // y of tile i, whose inputs are `before`
-        auto outputs = [&](int i) {
+        // y of tile i
+        auto outputs = [&](int i, auto odd) {
+            const Kept& before = kept[odd()];
             float y[K][4];
 #pragma unroll
             for (int k = 0; k < K; ++k) {
@@ -136,7 +132,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
                 for (int e = 0; e < 4; ++e) y[k][e] = skip[e] * widen(before.x[k].e[e]);
 #pragma unroll
                 for (int w = 0; w < NW; ++w) {
-                    const float4 v = *reinterpret_cast<const float4*>(&part[i & 1][w][row][mine.at]);
+                    const float4 v = *reinterpret_cast<const float4*>(&part[odd()][w][row][mine.at]);
                     y[k][0] += v.x, y[k][1] += v.y, y[k][2] += v.z, y[k][3] += v.w;
                 }
             }
@@ -163,22 +159,24 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
                 }
             });
         };
-        fetch(0);
-        inputs(0);
-        now = next;
-        if (tiles > 1) fetch(1);
+        const std::integral_constant<int, 0> even;
+        const std::integral_constant<int, 1> odd;
+        fetch(0, even);
+        fetch(1, odd);
+        inputs(0, even);
+        fetch(2, even);
         __syncthreads();
-        for (int i = 0; i < tiles; ++i) {
+        auto turn = [&](int i, auto other) {
             if constexpr (!MAPS) {
-                if (i > 0) outputs(i - 1);
-                before = now;
+                if (i > 0) outputs(i - 1, other);
             }
-            if (i + 1 < tiles) {
-                inputs(i + 1);
-                now = next;
-                if (i + 2 < tiles) fetch(i + 2);
-            }
+            inputs(i + 1, other);
+            fetch(i + 3, other);
             __syncthreads();
+        };
+        for (int i = 0; i < tiles; i += 2) {
+            turn(i, odd);
+            if (i + 1 < tiles) turn(i + 1, even);
         }
         if constexpr (MAPS) {
             // the sum of the steps, by channel; the last tile's are done with
@@ -187,7 +185,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
             for (int e = 0; e < 4; ++e) sums[mine.row * 64 + mine.at + e] = steps[e];
             __syncthreads();
         } else {
-            outputs(tiles - 1);
+            (tiles - 1) & 1 ? outputs(tiles - 1, odd) : outputs(tiles - 1, even);
         }
         return;
     }
@@ -215,26 +213,30 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
             }
         }
     }
-    SsmRegs<TIn, SN, kTile, VEC> nb, nc;
-    nb.place(l, n0, p.N, p.b_row);
-    nc.place(l, n0, p.N, p.c_row);
+    SsmRegs<TIn, SN, VEC> nb[2], nc[2];  // on their way, of tiles with even and with odd numbers
+#pragma unroll
+    for (int k = 0; k < 2; ++k) nb[k].place(l, n0, p.N, p.b_row), nc[k].place(l, n0, p.N, p.c_row);
     SsmStream bs(static_cast<const TIn*>(p.Bm) + me.g * p.N, token, p.b_row, p.N, kIn);
     SsmStream cs(static_cast<const TIn*>(p.Cm) + me.g * p.N, token, p.c_row, p.N, kIn);
-    auto fetch = [&](int i) {
+    auto fetch = [&](int i, auto odd) {
+        if (i >= tiles) return;
         const int valid = valid_of(i);
-        nb.load(bs.rows(valid));
-        if constexpr (!MAPS) nc.load(cs.rows(valid));
+        nb[odd()].load(bs.rows(valid));
+        if constexpr (!MAPS) nc[odd()].load(cs.rows(valid));
         bs.move(kTile), cs.move(kTile);
     };
-    fetch(0);
+    const std::integral_constant<int, 0> even;
+    const std::integral_constant<int, 1> odd;
+    fetch(0, even);
+    fetch(1, odd);
     bool dropped = false;
     __syncthreads();
-    for (int i = 0; i < tiles; ++i) {
+    auto turn = [&](int i, auto odd) {
         const int t0 = t_begin + i * kTile, valid = valid_of(i);
-        float B[1][SN], C[1][SN];
-        nb.get(B);
-        if constexpr (!MAPS) nc.get(C);
-        if (i + 1 < tiles) fetch(i + 1);
+        float B[SN], C[SN];
+        nb[odd()].get(B);
+        if constexpr (!MAPS) nc[odd()].get(C);
+        fetch(i + 2, odd);
         const uint64_t cuts = ssm_cuts(p, me.b, t0, valid, l);
         dropped = dropped || cuts != 0;
         if (!MAPS && p.saved && me.live) {
@@ -245,7 +247,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
                 if (n0 + n < p.N) to[static_cast<int64_t>(n0 + n) * p.D] = cuts & 1 ? 0.0f : h[n];
         }
         with_flag(cuts != 0, [&](auto with_cuts) {
-            const float(*from)[2][64] = du[i & 1];
+            const float(*from)[2][64] = du[odd()];
             float dn[2][4], un[2][4];  // steps and inputs of four tokens, and of the next four
 #pragma unroll
             for (int j = 0; j < 4; ++j) dn[0][j] = from[j][0][l], un[0][j] = from[j][1][l];
@@ -264,19 +266,23 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
                 float y[SN];
 #pragma unroll
                 for (int n = 0; n < SN; ++n) {
-                    h[n] = fmaf(__builtin_amdgcn_exp2f(step * A[n]), h[n], bcast<t>(B[0][n]) * u);
-                    if constexpr (!MAPS) y[n] = bcast<t>(C[0][n]) * h[n];
+                    h[n] = fmaf(__builtin_amdgcn_exp2f(step * A[n]), h[n], bcast<t>(B[n]) * u);
+                    if constexpr (!MAPS) y[n] = bcast<t>(C[n]) * h[n];
                 }
                 if constexpr (!MAPS) {
 #pragma unroll
                     for (int k = 1; k < SN; k *= 2)
 #pragma unroll
                         for (int n = 0; n < SN; n += 2 * k) y[n] += y[n + k];
-                    part[i & 1][wave][t][l] = y[0];
+                    part[odd()][wave][t][l] = y[0];
                 }
             });
         });
         __syncthreads();
+    };
+    for (int i = 0; i < tiles; i += 2) {
+        turn(i, even);
+        if (i + 1 < tiles) turn(i + 1, odd);
     }
     if constexpr (MAPS) {
         float* m = map_of<NP>(ws, chain, seg) + l;
