@@ -3,6 +3,7 @@
 #pragma once
 
 #include <type_traits>
+#include <utility>
 
 #include "osr_device.h"
 
@@ -126,6 +127,16 @@ __device__ __forceinline__ void with_flag(bool flag, F&& f) {
         f(std::true_type());
     else
         f(std::false_type());
+}
+
+// f(0), f(1) .. as compile-time constants.
+template <int... I, typename F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>()), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each_of(std::make_integer_sequence<int, N>(), f);
 }
 
 }  // namespace layer

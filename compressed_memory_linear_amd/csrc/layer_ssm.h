@@ -7,8 +7,6 @@
 // and channel (delta, u, the gate) through LDS and each sums its own states' part of y.
 #pragma once
 
-#include <utility>
-
 #include "layer_device.h"
 #include "layer_launch.h"
 
@@ -83,16 +81,6 @@ __device__ __forceinline__ uint64_t ssm_cuts(const SsmParams& p, int b, int t0, 
         cut = s[0] != s[-1];
     }
     return __ballot(cut);
-}
-
-// f(0), f(1) .. as compile-time constants.
-template <int... I, typename F>
-__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
-    (f(std::integral_constant<int, I>()), ...);
-}
-template <int N, typename F>
-__device__ __forceinline__ void each(F&& f) {
-    each_of(std::make_integer_sequence<int, N>(), f);
 }
 
 // B and C are the same for every channel of a group.  A register holds one state's values of 16 tokens, the same in
@@ -223,11 +211,14 @@ struct SsmSplit {
     int64_t chains, length;
     int segs;
 };
-inline SsmSplit ssm_split(const SsmParams& p) {
+#ifndef BWANT
+#define BWANT 1024
+#endif
+inline SsmSplit ssm_split(const SsmParams& p, bool backward) {
     SsmSplit s;
     s.chains = tiles_of(p.D / p.G, 64) * p.G * p.B;
     const int64_t waves = s.chains * (p.N <= 4 ? 1 : p.N <= 8 ? 2 : p.N <= 16 ? 4 : 8), tiles = tiles_of(p.T, kSsmTile);
-    int64_t want = waves > 704 ? 1 : 4096 / waves;
+    int64_t want = waves > 704 ? 1 : (backward ? BWANT : 4096) / waves;
     if (want > 64) want = 64;
     if (want > tiles / 4) want = tiles / 4;  // 64 tokens or more each
     if (want < 1) want = 1;

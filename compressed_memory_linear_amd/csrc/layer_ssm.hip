@@ -19,7 +19,7 @@ struct FwdSpace {
 };
 inline FwdSpace fwd_space(const SsmParams& p) {
     FwdSpace s;
-    const SsmSplit k = ssm_split(p);
+    const SsmSplit k = ssm_split(p, false);
     s.maps = static_cast<float*>(p.ws);
     s.segs = k.segs, s.length = k.length;
     s.bytes = s.segs > 1 ? static_cast<size_t>(k.chains) * s.segs * (ssm_padded(p.N) + 1) * 64 * sizeof(float) : 0;
@@ -302,60 +302,76 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
     }
 }
 
-// One token: L lanes to a channel, SN states each; state_out may be state_in (each value is read, then
-// written, by one lane).
-template <typename TIn, int L, int SN, bool VEC>
+// One token: L lanes to a channel, four states each, for NB sequences at a time; state_out may be state_in (each value
+// is read, then written, by one lane).
+template <typename TIn, int L, int NB, bool VEC>
 __global__ __launch_bounds__(256) void layer_ssm_step_kernel(SsmParams p) {
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t i = id / L;  // b D + c
-    const bool live = i < static_cast<int64_t>(p.B) * p.D;
-    const int b = live ? static_cast<int>(i / p.D) : 0, c = live ? static_cast<int>(i % p.D) : 0;
-    const int n0 = static_cast<int>(id % L) * SN, g = c / (p.D / p.G);
-    const TIn* Bm = static_cast<const TIn*>(p.Bm) + static_cast<int64_t>(b) * p.b_row + g * p.N;
-    const TIn* Cm = static_cast<const TIn*>(p.Cm) + static_cast<int64_t>(b) * p.c_row + g * p.N;
-    const float x = widen(static_cast<const TIn*>(p.x)[static_cast<int64_t>(b) * p.x_row + c]);
-    float d = widen(static_cast<const TIn*>(p.dt)[static_cast<int64_t>(b) * p.dt_row + c]) + (p.dt_bias ? p.dt_bias[c] : 0.0f);
-    float slope;
-    if (p.softplus) softplus_parts<kAccurate<TIn>>(d, d, slope);
-    const float u = d * x;
-    const int64_t s = (static_cast<int64_t>(b) * p.D + c) * p.N + n0, a = static_cast<int64_t>(c) * p.N + n0;
-    float y[1] = {0.0f}, h[SN], A[SN];
-    if (VEC && n0 < p.N) {
-        const auto hv = load_vec<float, SN>(p.state_in, s), av = load_vec<float, SN>(p.A, a);
-#pragma unroll
-        for (int n = 0; n < SN; ++n) h[n] = hv.e[n], A[n] = av.e[n];
-    } else {
-#pragma unroll
-        for (int n = 0; n < SN; ++n) {
-            h[n] = n0 + n < p.N ? p.state_in[s + n] : 0.0f;
-            A[n] = n0 + n < p.N ? p.A[a + n] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int n = 0; n < SN; ++n) {
-        const bool on = n0 + n < p.N;
-        h[n] = fmaf(__builtin_amdgcn_exp2f(d * (A[n] * kLog2e)), h[n], on ? u * widen(Bm[n0 + n]) : 0.0f);
-        if (on) y[0] = fmaf(widen(Cm[n0 + n]), h[n], y[0]);
-    }
-    if (live) {
-        if (VEC && n0 < p.N) {
-            store_vec<SN>(p.state_out, s, h, false);
+    const int c = static_cast<int>(blockIdx.x) * (256 / L) + threadIdx.x / L, n0 = threadIdx.x % L * 4;
+    if (c >= p.D) return;  // (with its whole group of L lanes)
+    const int left = p.N - n0;  // states from n0 on: none in the last lanes of some widths
+    const int g = c / (p.D / p.G);
+    const float bias = p.dt_bias ? p.dt_bias[c] : 0.0f, skip = p.skip ? p.skip[c] : 0.0f;
+    // four values at p, zeros past the last state
+    auto quad = [&](const auto* from) {
+        using T = std::remove_cv_t<std::remove_reference_t<decltype(*from)>>;
+        Vec<T, 4> v = {};
+        if (VEC) {
+            if (left > 0) v = load_vec<T, 4>(from, 0);
         } else {
 #pragma unroll
-            for (int n = 0; n < SN; ++n)
-                if (n0 + n < p.N) p.state_out[s + n] = h[n];
+            for (int n = 0; n < 4; ++n)
+                if (n < left) v.e[n] = from[n];
+        }
+        return v;
+    };
+    const Vec<float, 4> A = quad(p.A + static_cast<int64_t>(c) * p.N + n0);
+    for (int b0 = blockIdx.y * NB; b0 < p.B; b0 += gridDim.y * NB) {
+        Vec<float, 4> h[NB];
+        Vec<TIn, 4> B[NB], C[NB];
+        TIn x[NB], dt[NB], z[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            const int64_t b = min(b0 + i, p.B - 1);  // a sequence past the last: another's values, not stored
+            h[i] = quad(p.state_in + (b * p.D + c) * p.N + n0);
+            B[i] = quad(static_cast<const TIn*>(p.Bm) + b * p.b_row + g * p.N + n0);
+            C[i] = quad(static_cast<const TIn*>(p.Cm) + b * p.c_row + g * p.N + n0);
+            x[i] = static_cast<const TIn*>(p.x)[b * p.x_row + c];
+            dt[i] = static_cast<const TIn*>(p.dt)[b * p.dt_row + c];
+            if (p.z) z[i] = static_cast<const TIn*>(p.z)[b * p.z_row + c];
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            float d = widen(dt[i]) + bias, slope;
+            if (p.softplus) softplus_parts<kAccurate<TIn>>(d, d, slope);
+            const float u = d * widen(x[i]);
+            float y[1] = {0.0f}, o[4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                o[n] = fmaf(__builtin_amdgcn_exp2f(d * (A.e[n] * kLog2e)), h[i].e[n], u * widen(B[i].e[n]));
+                if (n < left) y[0] = fmaf(widen(C[i].e[n]), o[n], y[0]);
+            }
+            y[0] = osr::group_sum<L>(y[0]);
+            if (b0 + i >= p.B) continue;
+            const int64_t at = static_cast<int64_t>(b0 + i) * p.D + c;
+            float* to = p.state_out + at * p.N + n0;
+            if (VEC) {
+                if (left > 0) store_vec<4>(to, 0, o, false);
+            } else {
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    if (n < left) to[n] = o[n];
+            }
+            if (n0 != 0) continue;
+            y[0] = fmaf(skip, widen(x[i]), y[0]);
+            if (p.z) {
+                const float zv = widen(z[i]);
+                float s, r;
+                sigmoid2<kAccurate<TIn>>(zv, s, r);
+                y[0] *= zv * s;
+            }
+            store_vec<1>(p.y, at, y, p.y_bf16);
         }
     }
-    y[0] = osr::group_sum<L>(y[0]);
-    if (!live || n0 != 0) return;
-    if (p.skip) y[0] = fmaf(p.skip[c], x, y[0]);
-    if (p.z) {
-        const float z = widen(static_cast<const TIn*>(p.z)[static_cast<int64_t>(b) * p.z_row + c]);
-        float sg, r;
-        sigmoid2<kAccurate<TIn>>(z, sg, r);
-        y[0] *= z * sg;
-    }
-    store_vec<1>(p.y, i, y, p.y_bf16);
 }
 
 template <typename TIn>
@@ -377,20 +393,27 @@ void launch_fwd(const SsmParams& p, hipStream_t st) {
 
 template <typename TIn>
 void launch_step(const SsmParams& p, hipStream_t st) {
-    const bool vec = p.N % 4 == 0 && reinterpret_cast<uintptr_t>(p.state_in) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(p.state_out) % 16 == 0 && reinterpret_cast<uintptr_t>(p.A) % 16 == 0;
-    auto go = [&](auto L) {
-        const dim3 grid(static_cast<unsigned>(tiles_of(static_cast<int64_t>(p.B) * p.D * L(), 256)));
+    bool vec = p.N % 4 == 0 && p.b_row % 4 == 0 && p.c_row % 4 == 0;
+    for (const float* q : {p.state_in, static_cast<const float*>(p.state_out), p.A})
+        vec = vec && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+    for (const void* q : {p.Bm, p.Cm}) vec = vec && reinterpret_cast<uintptr_t>(q) % (4 * sizeof(TIn)) == 0;
+    auto go = [&](auto L, auto nb) {
+        const int64_t rows = tiles_of(p.B, nb());
+        const dim3 grid(static_cast<unsigned>(tiles_of(static_cast<int64_t>(p.D) * L(), 256)),
+                        static_cast<unsigned>(rows < 32768 ? rows : 32768));
         if (vec)
-            hipLaunchKernelGGL((layer_ssm_step_kernel<TIn, L(), 4, true>), grid, dim3(256), 0, st, p);
+            hipLaunchKernelGGL((layer_ssm_step_kernel<TIn, L(), nb(), true>), grid, dim3(256), 0, st, p);
         else
-            hipLaunchKernelGGL((layer_ssm_step_kernel<TIn, L(), 4, false>), grid, dim3(256), 0, st, p);
+            hipLaunchKernelGGL((layer_ssm_step_kernel<TIn, L(), nb(), false>), grid, dim3(256), 0, st, p);
     };
-    if (p.N <= 4) go(std::integral_constant<int, 1>());
-    else if (p.N <= 8) go(std::integral_constant<int, 2>());
-    else if (p.N <= 16) go(std::integral_constant<int, 4>());
-    else if (p.N <= 32) go(std::integral_constant<int, 8>());
-    else go(std::integral_constant<int, 16>());
+    auto by_batch = [&](auto L) {
+        p.B >= 16 ? go(L, std::integral_constant<int, 4>()) : go(L, std::integral_constant<int, 1>());
+    };
+    if (p.N <= 4) by_batch(std::integral_constant<int, 1>());
+    else if (p.N <= 8) by_batch(std::integral_constant<int, 2>());
+    else if (p.N <= 16) by_batch(std::integral_constant<int, 4>());
+    else if (p.N <= 32) by_batch(std::integral_constant<int, 8>());
+    else by_batch(std::integral_constant<int, 16>());
 }
 
 }  // namespace

@@ -30,7 +30,7 @@ struct BwdSpace {
 };
 inline BwdSpace bwd_space(const SsmParams& p) {
     BwdSpace s;
-    const SsmSplit k = ssm_split(p);
+    const SsmSplit k = ssm_split(p, true);
     s.segs = k.segs, s.length = k.length;
     const int64_t nbc = tiles_of(p.D / p.G, 64) * p.B * p.T * p.G * 2 * p.N;
     const int64_t ntok = static_cast<int64_t>(p.B) * s.segs * (p.N + 2) * p.D;

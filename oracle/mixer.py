@@ -197,7 +197,7 @@ def conv(x, w, bias=None, hist_in=None, act=SILU, lengths=None, segments=None, d
     if bias is not None:
         p, mag = p + bias.double(), mag + bias.double().abs()
     ep = (W + 1) * U * mag
-    phi, dphi, ephi, edphi = _silu(p) if act == SILU else (p, torch.ones_like(p), torch.zeros_like(p), torch.zeros_like(p))
+    phi, dphi, ephi, edphi = _silu(p, x.dtype == torch.bfloat16) if act == SILU else (p, torch.ones_like(p), torch.zeros_like(p), torch.zeros_like(p))
     n = torch.full((B,), T, device=dev) if lengths is None else lengths.to(dev).long().clamp(0, T)
     at = n[:, None] + torch.arange(W - 1, device=dev)  # the rows behind the last token
     alive = (torch.gather(doc, 1, at) == torch.gather(doc, 1, (n + W - 2)[:, None])) if W > 1 else at.bool()
