@@ -92,6 +92,8 @@ struct Shared {
     float part[Shape<NW>::kBuf][NW][kTile][2][64];  // du and ddelta of a wave's states
     float y[Shape<NW>::kBuf][NW][kTile][64];        // its part of C h
     float sums[Shape<NW>::kBuf][kTile][2 * SN * NW];  // dB and dC over the block
+    // what the outputs take of the inputs (x, z, dy, softplus'), where the same threads walk over states in between
+    float keep[Shape<NW>::kApart ? 1 : 4][Shape<NW>::kApart ? 1 : kTile][64];
 };
 
 // A segment of a chain, and its tiles from the last (0) to the first.
@@ -171,7 +173,6 @@ struct Taker {
     __device__ __forceinline__ void inputs(int i) {
         if (i >= s.tiles) return;
         const Raw& next = raw[B];
-        Kept& keep = kept[B];
         const int valid = s.valid(i);
         float d[K][4], slope[K][4], g[K][4];
 #pragma unroll
@@ -209,18 +210,44 @@ struct Taker {
                 (&dv.x)[e] = d[k][e];
                 (&uv.x)[e] = d[k][e] * widen(next.x[k].e[e]);
                 (&gv.x)[e] = g[k][e];
-                keep.d[k][e] = d[k][e], keep.slope[k][e] = slope[k][e];
             }
             *reinterpret_cast<float4*>(&sh.in[B][row][0][mine.at]) = dv;
             *reinterpret_cast<float4*>(&sh.in[B][row][1][mine.at]) = uv;
             *reinterpret_cast<float4*>(&sh.in[B][row][2][mine.at]) = gv;
-            keep.x[k] = next.x[k], keep.z[k] = next.z[k], keep.dy[k] = next.dy[k];
+            if constexpr (Sh::kApart) {
+                Kept& keep = kept[B];
+                keep.x[k] = next.x[k], keep.z[k] = next.z[k], keep.dy[k] = next.dy[k];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) keep.d[k][e] = d[k][e], keep.slope[k][e] = slope[k][e];
+            } else {
+                float4 v[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    (&v[0].x)[e] = widen(next.x[k].e[e]), (&v[1].x)[e] = widen(next.z[k].e[e]);
+                    (&v[2].x)[e] = widen(next.dy[k].e[e]), (&v[3].x)[e] = slope[k][e];
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float4*>(&sh.keep[j][row][mine.at]) = v[j];
+            }
+        }
+    }
+    // what inputs() kept for element e of quad k: x, z, dy, delta, softplus'
+    struct Was {
+        float x, z, dy, d, slope;
+    };
+    template <int B>
+    __device__ __forceinline__ Was was(int k, int e) const {
+        if constexpr (Sh::kApart) {
+            const Kept& keep = kept[B];
+            return Was{widen(keep.x[k].e[e]), widen(keep.z[k].e[e]), widen(keep.dy[k].e[e]), keep.d[k][e], keep.slope[k][e]};
+        } else {
+            const int row = mine.row + k * kStep, at = mine.at + e;
+            return Was{sh.keep[0][row][at], sh.keep[1][row][at], sh.keep[2][row][at], sh.in[B][row][0][at], sh.keep[3][row][at]};
         }
     }
     // the gradients of tile i, and the block's sums of B's and C's
     template <int B>
     __device__ __forceinline__ void outputs(int i) {
-        const Kept& keep = kept[B];
         const int valid = s.valid(i), rows = s.rows(i);
         float dx[K][4], ddt[K][4], dz[K][4];
 #pragma unroll
@@ -244,18 +271,19 @@ struct Taker {
             const bool on = row < valid;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float x = widen(keep.x[k].e[e]), dy = widen(keep.dy[k].e[e]);
+                const Was in = was<B>(k, e);
+                const float x = in.x, dy = in.dy;
                 float g = dy;
                 dz[k][e] = 0.0f;
                 if (p.z) {
-                    const float z = widen(keep.z[k].e[e]);
+                    const float z = in.z;
                     float sg, r;
                     sigmoid2<kAcc>(z, sg, r);
                     g *= z * sg;
                     dz[k][e] = dy * fmaf(skip[e], x, y[e]) * (sg * fmaf(z, r, 1.0f));
                 }
-                dx[k][e] = fmaf(du[e], keep.d[k][e], skip[e] * g);
-                ddt[k][e] = fmaf(du[e], x, q[e] * kLn2) * keep.slope[k][e];
+                dx[k][e] = fmaf(du[e], in.d, skip[e] * g);
+                ddt[k][e] = fmaf(du[e], x, q[e] * kLn2) * in.slope;
                 if (!on) dx[k][e] = ddt[k][e] = dz[k][e] = 0.0f;
                 if (on) {
                     dskip[e] = fmaf(g, x, dskip[e]);
@@ -288,7 +316,8 @@ template <typename TIn, int SN, int NW, bool VEC>
 struct Walker {
     using Sh = Shape<NW>;
     static constexpr int NP = SN * NW;
-    static constexpr int kPart = 64 / SN;    // tokens whose states and decays registers hold
+    static constexpr bool kHold = SN == 4;   // the decays too
+    static constexpr int kPart = 64 / SN;    // tokens whose states registers hold
     static constexpr int kPair = 8 / SN;     // tokens whose sums over the channels are taken together
     const SsmParams& p;
     Shared<SN, NW>& sh;
@@ -387,7 +416,7 @@ struct Walker {
             each<kParts>([&](auto pc) {
                 constexpr int first = (kParts - 1 - pc()) * kPart;
                 const float(&start)[SN] = first ? mid : before;
-                float h[kPart][SN], a[kPart][SN];
+                float h[kPart][SN], a[kHold ? kPart : 1][SN];
                 each<kPart>([&](auto tc) {
                     constexpr int i = tc(), t = first + i;
                     const float d = sh.in[B][t][0][l], u = sh.in[B][t][1][l];
@@ -396,8 +425,9 @@ struct Walker {
 #pragma unroll
                     for (int n = 0; n < SN; ++n) {
                         const float hp = i ? h[i ? i - 1 : 0][n] : start[n];
-                        a[i][n] = decay(d, n);
-                        h[i][n] = fmaf(a[i][n], cut ? 0.0f : hp, bcast<t>(Bv[n]) * u);
+                        const float e = decay(d, n);
+                        if constexpr (kHold) a[i][n] = e;
+                        h[i][n] = fmaf(e, cut ? 0.0f : hp, bcast<t>(Bv[n]) * u);
                         y[n] = bcast<t>(Cv[n]) * h[i][n];
                     }
                     if (p.z) {
@@ -425,7 +455,7 @@ struct Walker {
                             v[j * 2 * SN + SN + n] = g * h[i][n];
                             du[n] = bcast<t>(Bv[n]) * lam[n];
                             // a state that is dropped passes nothing back, whatever it was
-                            lam[n] = cut ? 0.0f : a[i][n] * lam[n];
+                            lam[n] = cut ? 0.0f : (kHold ? a[kHold ? i : 0][n] : decay(d, n)) * lam[n];
                             const float k = cut ? 0.0f : lam[n] * (i ? h[i ? i - 1 : 0][n] : start[n]);
                             q = fmaf(k, A[n], q);
                             dA[n] = fmaf(k, d, dA[n]);
