@@ -10,7 +10,8 @@ namespace {
 
 constexpr int kTile = kSsmTile;
 static_assert(kTile == 16 && kTile == kSsmSave, "a tile's B and C lie across 16 lanes, and a state is saved before each");
-// The workspace: the segments' maps [chain][segment][state, sum of steps][64].
+// The workspace: the segments' maps [chain][segment][state, sum of steps][64], of which the last is none: there lies the
+// state before the chain, since state_out may be where it was read and the segments start in any order.
 struct FwdSpace {
     float* maps;
     int segs;
@@ -197,9 +198,20 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
     for (int n = 0; n < SN; ++n) {
         const bool on = n0 + n < p.N;
         A[n] = on ? p.A[static_cast<int64_t>(c) * p.N + n0 + n] * kLog2e : 0.0f;
-        h[n] = !MAPS && on && p.state_in ? p.state_in[state + n] : 0.0f;
+        h[n] = on && p.state_in && (MAPS ? seg == 0 : ws.segs == 1) ? p.state_in[state + n] : 0.0f;
     }
-    if constexpr (!MAPS) {
+    if constexpr (MAPS) {
+        if (seg == 0) {
+            float* m = map_of<NP>(ws, chain, ws.segs - 1) + l;
+#pragma unroll
+            for (int n = 0; n < SN; ++n) m[(n0 + n) * 64] = h[n], h[n] = 0.0f;
+        }
+    } else {
+        if (ws.segs > 1) {
+            const float* m = map_of<NP>(ws, chain, ws.segs - 1) + l;
+#pragma unroll
+            for (int n = 0; n < SN; ++n) h[n] = m[(n0 + n) * 64];
+        }
         for (int k = 0; k < seg; ++k) {
             const float* m = map_of<NP>(ws, chain, k) + l;
             const float S = m[NP * 64];

@@ -895,6 +895,8 @@ def _row(name, t, shape, dtype, dev, inner):
     device: t is [B,T,...] whose last `inner` dimensions are contiguous and whose rows
     are one stride apart, as a slice of the last dimension of a contiguous tensor is."""
     if t.is_contiguous():
+        if t.shape == shape and t.dtype is dtype and t.device == dev:
+            return 0
         _check_tensor(name, t, shape, dtype, dev)
         return 0
     if tuple(t.shape) != tuple(shape):
@@ -921,10 +923,11 @@ def _lead(name, x):
         raise ValueError(f"{name} is [B,T,D] or [B,T,H,d]")
     if x.dtype not in _DT:
         raise ValueError("inputs must be float32 or bfloat16")
-    D = x.shape[2] if x.dim() == 3 else x.shape[2] * x.shape[3]
-    if max(x.shape[0], x.shape[1], D) > 2 ** 31 - 1:
+    B, T, *tok = x.shape
+    D = tok[0] if len(tok) == 1 else tok[0] * tok[1]
+    if B > 2 ** 31 - 1 or T > 2 ** 31 - 1 or D > 2 ** 31 - 1:
         raise ValueError(f"shape {tuple(x.shape)}: sizes are at most 2^31 - 1")
-    return x.shape[0], x.shape[1], D, tuple(x.shape[2:])
+    return B, T, D, tuple(tok)
 
 
 def _check_tokens(lengths, segments, B, T, dev):
@@ -938,6 +941,12 @@ def _check_dtypes(*dtypes):
     for dt in dtypes:
         if dt not in _DT:
             raise ValueError("tensors must be float32 or bfloat16")
+
+
+@functools.lru_cache(maxsize=1024)
+def _ref(kind, fields):
+    """A reference to the descriptor of these fields, which the library only reads."""
+    return ctypes.byref(kind(*fields))
 
 
 def make_conv_desc(B, T, D, W, act=CONV_SILU, in_dtype=BF16, y_dtype=BF16, grad_dtype=F32, x_row=0):
@@ -959,7 +968,7 @@ def _conv_desc(x, w, bias, hist_in, act, lengths, segments, y_dtype, grad_dtype)
     _check_tensor("w", w, tok + (W,), torch.float32, dev)
     if bias is not None:
         _check_tensor("bias", bias, tok, torch.float32, dev)
-    row = _row("x", x, x.shape, None, None, len(tok))
+    row = 0 if x.is_contiguous() else _row("x", x, x.shape, None, None, len(tok))
     hshape = (B, W - 1) + tok
     if hist_in is not None:
         _check_tensor("hist_in", hist_in, hshape, x.dtype, dev)
@@ -991,8 +1000,7 @@ def lattice_osr_conv_fwd(x, w, bias=None, hist_in=None, *, act: int = CONV_SILU,
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         ho = x.new_empty(hshape) if hist_out is None and history else hist_out
-        desc = lattice_osr_conv_desc(*fields)
-        rc = lib.lattice_osr_conv_fwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
+        rc = lib.lattice_osr_conv_fwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
                                       _ptr(hist_in), _ptr(ho), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_conv_fwd")
@@ -1031,8 +1039,7 @@ def lattice_osr_conv_bwd(x, w, dy, bias=None, hist_in=None, dhist_out=None, *, a
     def call(st):
         g = _grads(grads, want, x)
         ws, wbytes = _room(workspace, _conv_size(fields), x)
-        desc = lattice_osr_conv_desc(*fields)
-        rc = lib.lattice_osr_conv_bwd(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
+        rc = lib.lattice_osr_conv_bwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
                                       _ptr(hist_in), _ptr(dy), _ptr(dhist_out), _ptr(g["dx"]), _ptr(g["dw"]),
                                       _ptr(g.get("dbias")), _ptr(g.get("dhist_in")), _ptr(ws), wbytes, st)
         if rc != OK:
@@ -1061,8 +1068,7 @@ def lattice_osr_conv_step(x, w, hist_in, bias=None, *, act: int = CONV_SILU, y_d
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         ho = torch.empty_like(hist_in) if hist_out is None else hist_out
-        desc = lattice_osr_conv_desc(*fields)
-        rc = lib.lattice_osr_conv_step(ctypes.byref(desc), _ptr(x), _ptr(w), _ptr(bias), _ptr(hist_in), _ptr(ho),
+        rc = lib.lattice_osr_conv_step(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(hist_in), _ptr(ho),
                                        _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_conv_step")
@@ -1111,7 +1117,7 @@ def _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, lengths, segments, y_dtyp
         if t is not None:
             _check_tensor(name, t, tok, torch.float32, dev)
     k = len(tok)
-    rows = [_row("x", x, x.shape, None, None, k), _row("dt", dt, x.shape, dtype, dev, k),
+    rows = [0 if x.is_contiguous() else _row("x", x, x.shape, None, None, k), _row("dt", dt, x.shape, dtype, dev, k),
             _row("z", z, x.shape, dtype, dev, k) if z is not None else 0]
     if B.dim() not in (3, 4):
         raise ValueError("B and C are [B,T,N] or [B,T,G,N]")
@@ -1153,8 +1159,7 @@ def lattice_osr_ssm_fwd(x, dt, A, B, C, state_in=None, *, D=None, z=None, dt_bia
         snb, wnb, _ = _ssm_sizes(fields)
         sv, sbytes = _room(saved, snb, x) if save else (None, 0)
         ws, wbytes = _room(workspace, wnb, x)
-        desc = lattice_osr_ssm_desc(*fields)
-        rc = lib.lattice_osr_ssm_fwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+        rc = lib.lattice_osr_ssm_fwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                                      _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(state_in), _ptr(so), _ptr(yy),
                                      _ptr(sv), sbytes, _ptr(ws), wbytes, st)
         if rc != OK:
@@ -1192,8 +1197,7 @@ def lattice_osr_ssm_bwd(x, dt, A, B, C, dy, dstate_out=None, *, saved, D=None, z
         g = _grads(grads, want, x)
         sv, sbytes = _workspace(saved, 0, dev)
         ws, wbytes = _room(workspace, _ssm_sizes(fields)[2], x)
-        desc = lattice_osr_ssm_desc(*fields)
-        rc = lib.lattice_osr_ssm_bwd(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
+        rc = lib.lattice_osr_ssm_bwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
                                      _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(sv), sbytes, _ptr(dy),
                                      _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]),
                                      _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")), _ptr(g.get("ddt_bias")),
@@ -1222,8 +1226,7 @@ def lattice_osr_ssm_step(x, dt, A, B, C, state_in, *, D=None, z=None, dt_bias=No
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         so = torch.empty_like(state_in) if state_out is None else state_out
-        desc = lattice_osr_ssm_desc(*fields)
-        rc = lib.lattice_osr_ssm_step(ctypes.byref(desc), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
+        rc = lib.lattice_osr_ssm_step(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
                                       _ptr(z), _ptr(dt_bias), _ptr(state_in), _ptr(so), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_ssm_step")
@@ -1285,8 +1288,7 @@ def lattice_osr_layernorm_fwd(x, y=None, *, w=None, b=None, eps: float = 1e-5, z
     def call(st):
         xo = torch.empty_like(x) if x_out is None and y is not None else x_out
         zz = torch.empty_like(x, dtype=in_dtype) if z is None else z
-        desc = lattice_osr_layernorm_desc(*fields)
-        rc = lib.lattice_osr_layernorm_fwd(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(w), _ptr(b), _ptr(xo), _ptr(zz),
+        rc = lib.lattice_osr_layernorm_fwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w), _ptr(b), _ptr(xo), _ptr(zz),
                                            st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_layernorm_fwd")
@@ -1322,8 +1324,7 @@ def lattice_osr_layernorm_bwd(x, y=None, dx_out=None, dz=None, *, w=None, b=None
         g = _grads(grads, want, x)
         sums = w is not None or b is not None
         ws, wbytes = _room(workspace, _layernorm_size(fields) if sums else 0, x)
-        desc = lattice_osr_layernorm_desc(*fields)
-        rc = lib.lattice_osr_layernorm_bwd(ctypes.byref(desc), _ptr(x), _ptr(y), _ptr(w), _ptr(dx_out), _ptr(dz),
+        rc = lib.lattice_osr_layernorm_bwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w), _ptr(dx_out), _ptr(dz),
                                            _ptr(g["dx"]), _ptr(g.get("dy")), _ptr(g.get("dw")), _ptr(g.get("db")),
                                            _ptr(ws), wbytes, st)
         if rc != OK:

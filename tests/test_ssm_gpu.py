@@ -480,3 +480,37 @@ def test_gradient_by_differences():
         exact = loss(ref, up) - loss(ref, down)
         assert abs(exact - slope) <= 0.02 * max(abs(slope), scale), n
         assert abs(loss(lambda a: forward(a), up) - loss(lambda a: forward(a), down) - slope) <= 0.025 * max(abs(slope), scale), n
+
+
+def test_offsets_past_32_bits():
+    """Rows so far apart that the last ones lie more than 2^32 bytes behind the first, and a `saved` of more than 2^32
+    bytes: the same as a contiguous copy's, and as the calls' on the last tokens alone from the state before them."""
+    T, D, N, wide = 70000, 64, 16, 65536
+    x = make(1, T, D, N, seed=61)
+    big = torch.empty((1, T, wide), dtype=BF, device="cuda")
+    v = dict(x, z=big[..., 100:100 + D], x=big[..., wide - D:])
+    v["z"].copy_(x["z"])
+    v["x"].copy_(x["x"])
+    a, b = forward(x), forward(v)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    del big, v
+    T, D = 2100, 16384 * 32
+    x = make(1, T, D, N, seed=62, state=False)
+    y, st, sv = forward(x, save=True, y_dtype=BF)
+    assert sv.numel() > 2 ** 32
+    dy = torch.randn((1, T, D), device="cuda").to(BF)
+    g = backward(x, dy, None, sv, grad_dtype=BF)
+    cut, cols = 2048, slice(D - 64, D)
+    part = {k: t[:, cut:].contiguous() if k in ("x", "dt", "z", "B", "C") else t for k, t in x.items() if t is not None}
+    part = {k: t[..., cols].contiguous() if k in ("x", "dt", "z", "D", "dt_bias") else t for k, t in part.items()}
+    part["A"] = x["A"][cols].contiguous()
+    head = {k: t[:, :cut].contiguous() if k in ("B", "C") else t[:, :cut, cols].contiguous() if k in ("x", "dt", "z") else part[k]
+            for k, t in x.items() if t is not None}
+    head["state_in"] = None
+    _, before = forward(head)
+    out, bound = mixer.ssm(part["x"], part["dt"], part["A"], part["B"], part["C"], before, part["D"], part["z"],
+                           part["dt_bias"], dy=dy[:, cut:, cols], dstate_out=None)
+    check("y", y[:, cut:, cols].contiguous(), out["y"], bound["y"])
+    check("state", st[:, cols].contiguous(), out["state_out"], bound["state_out"])
+    for k in ("dx", "ddt", "dz"):
+        check(k, g[k][:, cut:, cols].contiguous(), out[k], bound[k])
