@@ -5,6 +5,10 @@
 // Rows lie in registers as for the other norms (layer_norm.h): read once, the variance taken from
 // the differences.  The backward takes the forward again from x and y, so that nothing of it is kept; its sums
 // over rows stay with each thread's columns, go to the workspace and are added in a fixed order.
+//
+// Bound by HBM: R32768 D2048 bf16 with the residual, forward 537 MB in 86 us, 6.2 TB/s (part of it from the 256 MB cache),
+// backward 671 MB in 119 us, 5.6 TB/s, and 5 us for the sums.  R2331 D1001 (odd rows, element by element, residual
+// in fp32): 11 us for 29 MB, one to two rows to a workgroup and two sums over their waves; the sums 4 us.
 #include "layer_norm.h"
 
 namespace layer {

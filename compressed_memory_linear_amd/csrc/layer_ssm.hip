@@ -3,6 +3,15 @@
 // Where the chains of 64 channels are too few to fill the device the time axis is split into segments: a first kernel
 // takes every segment but the last from a state of zeros to its end, which gives the segment's map h -> exp(A S) h + H
 // (S the sum of its steps); the second starts each segment from the maps before it, composed in order.
+//
+// Bound by the vector units: a state and token takes a product, an exponential (two slots), B's product, the state's step
+// and 1.75 operations for y, 4 cycles each for 64 channels; another 36 to 40 instructions per token and 64 channels
+// are softplus, gate, conversions and the sum over waves.  D2048 N16 bf16: B8 T4096 (one segment) 292 to 320 us, the
+// units 92 % busy, 0.54 GB of 100 us; B1 T65536 (32 segments) 865 us, of which the maps are 40 %, the units
+// busy throughout.  From a wave for all 16 states and B and C in LDS, a tile at a time (1099 and 17400 us): segments, B and C by lane
+// broadcast, quads 433 and 1430; addresses kept, steps four tokens ahead 395; inputs and outputs by waves of their own 390 and
+// 920; loads two tiles ahead 320 and 870.  Two states to a lane and twice the waves: 332 and 1071 with one
+// and 8 segments, against 317 and 1049.
 #include "layer_ssm.h"
 
 namespace layer {
@@ -315,7 +324,8 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
 }
 
 // One token: L lanes to a channel, four states each, for NB sequences at a time; state_out may be state_in (each value
-// is read, then written, by one lane).
+// is read, then written, by one lane).  Bound by HBM: B256 D4096 N16 moves 142 MB in 24 us (one sequence at a time and
+// 64-bit divisions for its place: 43); four sequences from 16 on, one below, where workgroups are few.
 template <typename TIn, int L, int NB, bool VEC>
 __global__ __launch_bounds__(256) void layer_ssm_step_kernel(SsmParams p) {
     const int c = static_cast<int>(blockIdx.x) * (256 / L) + threadIdx.x / L, n0 = threadIdx.x % L * 4;

@@ -1000,8 +1000,8 @@ def lattice_osr_conv_fwd(x, w, bias=None, hist_in=None, *, act: int = CONV_SILU,
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         ho = x.new_empty(hshape) if hist_out is None and history else hist_out
-        rc = lib.lattice_osr_conv_fwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
-                                      _ptr(hist_in), _ptr(ho), _ptr(yy), st)
+        rc = lib.lattice_osr_conv_fwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths),
+                                      _ptr(segments), _ptr(hist_in), _ptr(ho), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_conv_fwd")
         return (yy, ho) if history else yy
@@ -1039,9 +1039,10 @@ def lattice_osr_conv_bwd(x, w, dy, bias=None, hist_in=None, dhist_out=None, *, a
     def call(st):
         g = _grads(grads, want, x)
         ws, wbytes = _room(workspace, _conv_size(fields), x)
-        rc = lib.lattice_osr_conv_bwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths), _ptr(segments),
-                                      _ptr(hist_in), _ptr(dy), _ptr(dhist_out), _ptr(g["dx"]), _ptr(g["dw"]),
-                                      _ptr(g.get("dbias")), _ptr(g.get("dhist_in")), _ptr(ws), wbytes, st)
+        rc = lib.lattice_osr_conv_bwd(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(lengths),
+                                      _ptr(segments), _ptr(hist_in), _ptr(dy), _ptr(dhist_out), _ptr(g["dx"]),
+                                      _ptr(g["dw"]), _ptr(g.get("dbias")), _ptr(g.get("dhist_in")), _ptr(ws), wbytes,
+                                      st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_conv_bwd")
         return g
@@ -1068,8 +1069,8 @@ def lattice_osr_conv_step(x, w, hist_in, bias=None, *, act: int = CONV_SILU, y_d
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         ho = torch.empty_like(hist_in) if hist_out is None else hist_out
-        rc = lib.lattice_osr_conv_step(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias), _ptr(hist_in), _ptr(ho),
-                                       _ptr(yy), st)
+        rc = lib.lattice_osr_conv_step(_ref(lattice_osr_conv_desc, fields), _ptr(x), _ptr(w), _ptr(bias),
+                                       _ptr(hist_in), _ptr(ho), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_conv_step")
         return yy, ho
@@ -1159,9 +1160,9 @@ def lattice_osr_ssm_fwd(x, dt, A, B, C, state_in=None, *, D=None, z=None, dt_bia
         snb, wnb, _ = _ssm_sizes(fields)
         sv, sbytes = _room(saved, snb, x) if save else (None, 0)
         ws, wbytes = _room(workspace, wnb, x)
-        rc = lib.lattice_osr_ssm_fwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                     _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(state_in), _ptr(so), _ptr(yy),
-                                     _ptr(sv), sbytes, _ptr(ws), wbytes, st)
+        rc = lib.lattice_osr_ssm_fwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
+                                     _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(state_in),
+                                     _ptr(so), _ptr(yy), _ptr(sv), sbytes, _ptr(ws), wbytes, st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_ssm_fwd")
         return (yy, so, sv) if save else (yy, so)
@@ -1197,11 +1198,11 @@ def lattice_osr_ssm_bwd(x, dt, A, B, C, dy, dstate_out=None, *, saved, D=None, z
         g = _grads(grads, want, x)
         sv, sbytes = _workspace(saved, 0, dev)
         ws, wbytes = _room(workspace, _ssm_sizes(fields)[2], x)
-        rc = lib.lattice_osr_ssm_bwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D), _ptr(z),
-                                     _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(sv), sbytes, _ptr(dy),
-                                     _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]), _ptr(g["dB"]),
-                                     _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")), _ptr(g.get("ddt_bias")),
-                                     _ptr(g["dstate_in"]), _ptr(ws), wbytes, st)
+        rc = lib.lattice_osr_ssm_bwd(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
+                                     _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(lengths), _ptr(segments), _ptr(sv), sbytes,
+                                     _ptr(dy), _ptr(dstate_out), _ptr(g["dx"]), _ptr(g["ddt"]), _ptr(g["dA"]),
+                                     _ptr(g["dB"]), _ptr(g["dC"]), _ptr(g.get("dD")), _ptr(g.get("dz")),
+                                     _ptr(g.get("ddt_bias")), _ptr(g["dstate_in"]), _ptr(ws), wbytes, st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_ssm_bwd")
         return g
@@ -1226,8 +1227,8 @@ def lattice_osr_ssm_step(x, dt, A, B, C, state_in, *, D=None, z=None, dt_bias=No
     def call(st):
         yy = x.new_empty(x.shape, dtype=y_dtype) if y is None else y
         so = torch.empty_like(state_in) if state_out is None else state_out
-        rc = lib.lattice_osr_ssm_step(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C), _ptr(D),
-                                      _ptr(z), _ptr(dt_bias), _ptr(state_in), _ptr(so), _ptr(yy), st)
+        rc = lib.lattice_osr_ssm_step(_ref(lattice_osr_ssm_desc, fields), _ptr(x), _ptr(dt), _ptr(A), _ptr(B), _ptr(C),
+                                      _ptr(D), _ptr(z), _ptr(dt_bias), _ptr(state_in), _ptr(so), _ptr(yy), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_ssm_step")
         return yy, so
@@ -1288,8 +1289,8 @@ def lattice_osr_layernorm_fwd(x, y=None, *, w=None, b=None, eps: float = 1e-5, z
     def call(st):
         xo = torch.empty_like(x) if x_out is None and y is not None else x_out
         zz = torch.empty_like(x, dtype=in_dtype) if z is None else z
-        rc = lib.lattice_osr_layernorm_fwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w), _ptr(b), _ptr(xo), _ptr(zz),
-                                           st)
+        rc = lib.lattice_osr_layernorm_fwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w),
+                                           _ptr(b), _ptr(xo), _ptr(zz), st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_layernorm_fwd")
         return xo, zz
@@ -1300,8 +1301,8 @@ def lattice_osr_layernorm_fwd(x, y=None, *, w=None, b=None, eps: float = 1e-5, z
 def lattice_osr_layernorm_bwd(x, y=None, dx_out=None, dz=None, *, w=None, b=None, eps: float = 1e-5, grad_dtype=None,
                               grads: Optional[dict] = None, workspace=None, stream=None) -> dict:
     """Gradients of sum(dx_out*x_out) + sum(dz*z) of lattice_osr_layernorm_fwd with the same inputs.  dx_out (x's
-    dtype; None: zeros) and dz (y's dtype) have x's shape.  Returns a dict of dx (x's dtype), dy with y (grad_dtype, y's dtype
-    if that is None; dx itself where that is x's dtype), dw and db (float32, where w and b were passed),
+    dtype; None: zeros) and dz (y's dtype) have x's shape.  Returns a dict of dx (x's dtype), dy with y (grad_dtype,
+    y's dtype if that is None; dx itself where that is x's dtype), dw and db (float32, where w and b were passed),
     allocated unless passed in `grads` (dx may be dx_out)."""
     lib = load_library()
     if dz is None:
@@ -1324,9 +1325,9 @@ def lattice_osr_layernorm_bwd(x, y=None, dx_out=None, dz=None, *, w=None, b=None
         g = _grads(grads, want, x)
         sums = w is not None or b is not None
         ws, wbytes = _room(workspace, _layernorm_size(fields) if sums else 0, x)
-        rc = lib.lattice_osr_layernorm_bwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w), _ptr(dx_out), _ptr(dz),
-                                           _ptr(g["dx"]), _ptr(g.get("dy")), _ptr(g.get("dw")), _ptr(g.get("db")),
-                                           _ptr(ws), wbytes, st)
+        rc = lib.lattice_osr_layernorm_bwd(_ref(lattice_osr_layernorm_desc, fields), _ptr(x), _ptr(y), _ptr(w),
+                                           _ptr(dx_out), _ptr(dz), _ptr(g["dx"]), _ptr(g.get("dy")), _ptr(g.get("dw")),
+                                           _ptr(g.get("db")), _ptr(ws), wbytes, st)
         if rc != OK:
             raise OSRError(rc, "lattice_osr_layernorm_bwd")
         if y is not None and not own_dy:
