@@ -207,22 +207,28 @@ __host__ __device__ inline int ssm_padded(int N) { return N <= 4 ? 4 : N <= 8 ? 
 // segment twice costs more; else as many as fill it, and hide one another's waits.
 // Forward, by the waves that walk over states for 1024 vector units (D2048 N16 bf16): B8 T4096 (1024 waves) 1 segment
 // 321 us, 3 411; B1 T65536 (128 waves) 8 segments 1051, 24 876, 32 867; B7 T1531 D1001 N13 padded fp32 (448 waves) 2
-// 149, 6 130, 9 122.  Backward, by workgroups, of which a compute unit's LDS holds one past 8 states: training step of
-// B4 T4096 D2048 N16 (128 chains) 2 segments 1000 us, 4 970, 8 980; B3 T777 D514 N64 (30 chains) 4 749, 8 529, 12 597.
+// 149, 6 130, 9 122.  Past 32 states a wave holds twice as many: training step of B3 T777 D514 N64 with 7 segments
+// forward 427 us, 10 471.  Backward, by workgroups, of which a compute unit's LDS holds one past 8 states: training step
+// of B4 T4096 D2048 N16 (128 chains) 2 segments 1000 us, 4 970, 8 980; B3 T777 D514 N64 (30 chains) 4 749, 8 529, 12 597.
+// The kernel of its maps has smaller workgroups and takes long segments in four parts (B4 T4096, 64 tiles a segment:
+// 128 -> 95 us), short ones whole, since each segment reads the maps of all parts behind it (the training step of
+// B3 T777, 7 tiles a segment: whole 393 us, in four parts 427).
 struct SsmSplit {
     int64_t chains, length;
-    int segs;
+    int segs, parts;  // parts of a segment, each with a map of its own
 };
 inline SsmSplit ssm_split(const SsmParams& p, bool backward) {
     SsmSplit s;
     s.chains = tiles_of(p.D / p.G, 64) * p.G * p.B;
     const int64_t waves = s.chains * (p.N <= 4 ? 1 : p.N <= 8 ? 2 : p.N <= 16 ? 4 : 8), tiles = tiles_of(p.T, kSsmTile);
-    int64_t want = waves > 704 ? 1 : 4096 / waves;
+    int64_t want = waves > 704 ? 1 : (p.N <= 32 ? 4096 : 2048) / waves;
     if (backward) want = s.chains > 176 ? 1 : (p.N <= 16 ? 512 : 256) / s.chains;
     if (want > 64) want = 64;
     if (want > tiles / 4) want = tiles / 4;  // 64 tokens or more each
     if (want < 1) want = 1;
-    const int per = static_cast<int>(tiles_of(tiles, static_cast<int>(want)));
+    int per = static_cast<int>(tiles_of(tiles, static_cast<int>(want)));
+    s.parts = backward && want > 1 && per >= 16 ? 4 : 1;
+    per = static_cast<int>(tiles_of(per, s.parts)) * s.parts;
     s.length = static_cast<int64_t>(per) * kSsmTile;
     s.segs = static_cast<int>(tiles_of(tiles, per));
     return s;

@@ -16,9 +16,9 @@
 // Bound by the vector units, one wave that walks over states and one that takes inputs and outputs to each (256
 // registers; 127 KB of LDS at 16 states): B4 T4096 D2048 N16 bf16, 4 segments, 560 to 640 us, the units 75 % busy.  Of about 22
 // instructions per state and token six take the state again, nine are the gradients' and five the sums over
-// channels, which permlane swaps of 8 cycles make 94 of 350 cycles per token and four states.  The maps in front 100 to 130 us, the
+// channels, which permlane swaps of 8 cycles make 94 of 350 cycles per token and four states.  The maps in front 95 us, the
 // kernels behind 14 and 8.  (The whole training step: 4825 us with one wave's sums over 64 lanes one by one, one
-// segment and nothing ahead; 980 so.)  64 states (B3 T777 D514 fp32) spill 131 to 153 registers: 248 us,
+// segment and nothing ahead; 945 so.)  64 states (B3 T777 D514 fp32) spill 131 to 153 registers: 248 us,
 // with the decays held too 334, in one part of 16 tokens 400.
 #pragma once
 
@@ -31,20 +31,24 @@ constexpr int kTile = kSsmSave;
 static_assert(kTile == 16, "a tile's B and C lie across 16 lanes");
 
 // The workspace: sums of B's and C's gradients [block][B T][G][2][N], those over tokens [B][segment][N + 2][D] (dA,
-// dskip, ddt_bias), the segments' maps [chain][segment][state, sum of steps][64].
+// dskip, ddt_bias), the maps [chain][part of a segment][state, sum of steps][64].  Those are formed by a kernel of small
+// workgroups, for which the main kernel's segments are too few: a segment has several of them.
 struct BwdSpace {
     float *bc, *tok, *maps;
-    int segs;
-    int64_t length;  // tokens per segment, whole tiles
+    int segs, parts, per;  // segments of a chain, parts of all of them, parts of a segment
+    int64_t length;        // tokens per segment, whole tiles
+    int64_t part_length;
     size_t bytes;
 };
 inline BwdSpace bwd_space(const SsmParams& p) {
     BwdSpace s;
     const SsmSplit k = ssm_split(p, true);
     s.segs = k.segs, s.length = k.length;
+    s.per = k.parts, s.part_length = k.length / k.parts;
+    s.parts = static_cast<int>((p.T + s.part_length - 1) / s.part_length);
     const int64_t nbc = tiles_of(p.D / p.G, 64) * p.B * p.T * p.G * 2 * p.N;
     const int64_t ntok = static_cast<int64_t>(p.B) * s.segs * (p.N + 2) * p.D;
-    const int64_t nmap = s.segs > 1 ? k.chains * s.segs * (ssm_padded(p.N) + 1) * 64 : 0;
+    const int64_t nmap = s.segs > 1 ? k.chains * s.parts * (ssm_padded(p.N) + 1) * 64 : 0;
     s.bc = static_cast<float*>(p.ws);
     s.tok = s.bc + nbc;
     s.maps = s.tok + ntok;
@@ -53,7 +57,7 @@ inline BwdSpace bwd_space(const SsmParams& p) {
 }
 template <int NP>
 __device__ __forceinline__ float* map_of(const BwdSpace& ws, int chain, int k) {
-    return ws.maps + (static_cast<int64_t>(chain) * ws.segs + k) * (NP + 1) * 64;
+    return ws.maps + (static_cast<int64_t>(chain) * ws.parts + k) * (NP + 1) * 64;
 }
 
 // Sixteen sums over the lanes at once, each step halving the registers: 35 operations where one by one they take 96.
@@ -111,11 +115,11 @@ struct Segment {
     __device__ __forceinline__ int rows(int i) const { return min(kTile, t_end - t0(i)); }
     __device__ __forceinline__ int valid(int i) const { return min(len - t0(i), rows(i)); }
 };
-__device__ __forceinline__ Segment segment_of(const SsmParams& p, const BwdSpace& ws, int len, int chains) {
+__device__ __forceinline__ Segment segment_of(const SsmParams& p, int seg, int64_t length, int len, int chains) {
     Segment s;
-    s.chain = blockIdx.x % chains, s.seg = blockIdx.x / chains;
-    s.t_begin = static_cast<int>(s.seg * ws.length);
-    s.t_end = static_cast<int>(min(s.t_begin + ws.length, static_cast<int64_t>(p.T)));
+    s.chain = blockIdx.x % chains, s.seg = seg;
+    s.t_begin = static_cast<int>(seg * length);
+    s.t_end = static_cast<int>(min(s.t_begin + length, static_cast<int64_t>(p.T)));
     s.tiles = (s.t_end - s.t_begin + kTile - 1) / kTile;
     s.len = len, s.T = p.T;
     return s;
@@ -354,7 +358,7 @@ struct Walker {
             A[n] = on ? p.A[static_cast<int64_t>(c) * p.N + n0 + n] * kLog2e : 0.0f;
             lam[n] = on && me.live && p.dstate_out ? p.dstate_out[state + n] : 0.0f;
         }
-        for (int k = ws.segs - 1; k > s.seg; --k) {
+        for (int k = ws.parts - 1; k >= (s.seg + 1) * ws.per; --k) {
             const float* m = map_of<NP>(ws, s.chain, k) + l;
             const float S = m[NP * 64];
 #pragma unroll
@@ -498,7 +502,7 @@ __global__ __launch_bounds__(Shape<NW>::kNT) void layer_ssm_bwd_kernel(SsmParams
     __shared__ Shared<SN, NW> sh;
     const int chains = p.B * p.G * ssm_blocks(p);
     const SsmPlace me = ssm_place(p, blockIdx.x % chains);
-    const Segment s = segment_of(p, ws, me.len, chains);
+    const Segment s = segment_of(p, blockIdx.x / chains, ws.length, me.len, chains);
     float* tok = ws.tok + (static_cast<int64_t>(me.b) * ws.segs + s.seg) * (p.N + 2) * p.D;
     auto take_sums = [&](const Taker<TIn, TDy, SN, NW, VEC>& t) {
         // dskip and ddt_bias, of kHT / 16 threads each

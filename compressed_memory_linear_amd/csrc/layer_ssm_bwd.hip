@@ -6,7 +6,7 @@ namespace layer {
 namespace ssm_bwd {
 namespace {
 
-// The segments' maps, of all but the first: from a gradient of zeros behind each to the one in front of it.
+// The maps of the parts of all segments but the first: from a gradient of zeros behind each to the one in front of it.
 template <typename TIn, typename TDy, int SN, int NW, bool VEC>
 __global__ __launch_bounds__((NW + (NW < 4 ? 2 : 4)) * 64) void layer_ssm_bwd_maps_kernel(SsmParams p, BwdSpace ws) {
     constexpr int HT = (NW < 4 ? 2 : 4) * 64, K = kTile * 16 / HT, kStep = HT / 16, kIn = sizeof(TIn), NP = SN * NW;
@@ -14,11 +14,7 @@ __global__ __launch_bounds__((NW + (NW < 4 ? 2 : 4)) * 64) void layer_ssm_bwd_ma
     __shared__ float in[2][kTile][2][64];  // delta, g
     const int chains = p.B * p.G * ssm_blocks(p);
     const SsmPlace me = ssm_place(p, blockIdx.x % chains);
-    Segment s = segment_of(p, ws, me.len, chains);
-    s.seg += 1;
-    s.t_begin = static_cast<int>(s.seg * ws.length);
-    s.t_end = static_cast<int>(min(s.t_begin + ws.length, static_cast<int64_t>(p.T)));
-    s.tiles = (s.t_end - s.t_begin + kTile - 1) / kTile;
+    const Segment s = segment_of(p, ws.per + blockIdx.x / chains, ws.part_length, me.len, chains);
     const int64_t token = static_cast<int64_t>(me.b) * p.T + s.t0(0);
     const std::integral_constant<int, 0> even;
     const std::integral_constant<int, 1> odd;
@@ -184,7 +180,7 @@ void launch_maps(const SsmParams& p, const BwdSpace& ws, hipStream_t st) {
     with_states(p.N, [&](auto sn, auto nw) {
         const unsigned chains = static_cast<unsigned>(p.B) * p.G * tiles_of(p.D / p.G, 64);
         auto go = [&](auto vec) {
-            hipLaunchKernelGGL((layer_ssm_bwd_maps_kernel<TIn, TDy, sn(), nw(), vec()>), dim3(chains * (ws.segs - 1)),
+            hipLaunchKernelGGL((layer_ssm_bwd_maps_kernel<TIn, TDy, sn(), nw(), vec()>), dim3(chains * (ws.parts - ws.per)),
                                dim3((nw() + (nw() < 4 ? 2 : 4)) * 64), 0, st, p, ws);
         };
         ssm_vec(p) ? go(std::true_type()) : go(std::false_type());

@@ -349,9 +349,11 @@ def test_step(B, D, N, G, dtype, y_dtype):
 
 
 @pytest.mark.parametrize("B,T,D,N,G", [(1, 5000, 64, 16, 1), (1, 2500, 320, 16, 1), (2, 2100, 128, 32, 2),
-                                       (1, 1300, 130, 64, 1), (9, 600, 512, 16, 1)])
+                                       (1, 1300, 130, 64, 1), (9, 600, 512, 16, 1), (1, 1300, 6400, 4, 1),
+                                       (1, 1030, 4096, 33, 1)])
 def test_long_and_wide(B, T, D, N, G):
-    """Few channels over many tiles, and enough of them to fill the chip; ragged and packed."""
+    """Few channels over many tiles, and enough of them to fill the chip; segments long enough for several maps each;
+    ragged and packed."""
     g = torch.Generator(device="cuda").manual_seed(41)
     x = make(B, T, D, N, G, seed=41, step=0.01)
     n = torch.randint(0, T + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
