@@ -227,10 +227,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
 #pragma unroll
             for (int n = 0; n < SN; ++n) {
                 const float H = m[(n0 + n) * 64];
-                // a segment with a document's border in it passes nothing on, whatever it is; a product of decays that
-                // underflows is held above 0, so that an infinite state stays one as token by token
-                const float P = fmaxf(__builtin_amdgcn_exp2f(A[n] * S), 1.40129846e-45f);
-                h[n] = S == __builtin_inff() ? H : fmaf(P, h[n], H);
+                h[n] = ssm_across(A[n], S, h[n], H);
             }
         }
     }

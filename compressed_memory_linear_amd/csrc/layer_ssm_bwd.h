@@ -354,9 +354,10 @@ struct Walker {
         sum_at = -(v / (2 * SN)) * 2 * NP + v / SN % 2 * NP + n0 + v % SN;
 #pragma unroll
         for (int n = 0; n < SN; ++n) {
-            const bool on = n0 + n < p.N;
+            // (lanes past the last channel hold zeros throughout, since the sums over channels take them in)
+            const bool on = n0 + n < p.N && me.live;
             A[n] = on ? p.A[static_cast<int64_t>(c) * p.N + n0 + n] * kLog2e : 0.0f;
-            lam[n] = on && me.live && p.dstate_out ? p.dstate_out[state + n] : 0.0f;
+            lam[n] = on && p.dstate_out ? p.dstate_out[state + n] : 0.0f;
         }
         for (int k = ws.parts - 1; k >= (s.seg + 1) * ws.per; --k) {
             const float* m = map_of<NP>(ws, s.chain, k) + l;
@@ -364,8 +365,7 @@ struct Walker {
 #pragma unroll
             for (int n = 0; n < SN; ++n) {
                 const float R = m[(n0 + n) * 64];
-                const float P = fmaxf(__builtin_amdgcn_exp2f(A[n] * S), 1.40129846e-45f);
-                lam[n] = S == __builtin_inff() ? R : fmaf(P, lam[n], R);
+                lam[n] = ssm_across(A[n], S, lam[n], R);
             }
         }
 #pragma unroll

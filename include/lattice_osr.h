@@ -627,7 +627,9 @@ LATTICE_OSR_API size_t lattice_osr_conv_bwd_workspace_bytes(const lattice_osr_co
  *   h_t[n] = exp(delta_t A[c,n]) h_{t-1}[n] + delta_t x_t B_t[n],
  *   y_t = (sum_n C_t[n] h_t[n] + skip[c] x_t) z_t sigmoid(z_t)
  * (no gate where z is NULL; skip, dt_bias NULL: zeros).  h_{-1} is state_in
- * (zeros where it is NULL).  Steps, decays, states and sums are fp32.
+ * (zeros where it is NULL).  Steps, decays, states and sums are fp32.  A is
+ * finite, of either sign.  What depends on a value that is not finite is not
+ * finite, though it may be NaN where the formulas give an infinity.
  *   x, dt, z        [B, T, D]     in_dtype, rows x_row, dt_row, z_row apart
  *   Bm, Cm          [B, T, G, N]  in_dtype, rows b_row, c_row apart; channel c
  *                                 takes group c / (D / G)

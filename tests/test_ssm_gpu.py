@@ -214,6 +214,26 @@ def test_nan_stays_in_its_channel_and_behind():
     assert torch.equal(torch.isnan(st).all(-1), bad[:, -1]) and torch.equal(torch.isnan(st).any(-1), bad[:, -1])
 
 
+@pytest.mark.parametrize("D,N", [(66, 4), (130, 16), (64, 40)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_states_that_grow(D, N, dtype):
+    """A > 0.  A first document whose states and gradients are zeros while the product of its decays passes fp32's
+    range, and one of moderate growth; channels that do not fill the last block of 64."""
+    T, first = 400, 160
+    x = make(2, T, D, N, dtype=dtype, seed=20, bias=False, state=False, step=0.01)
+    x["A"] = torch.linspace(-2, 2, N, device="cuda").expand(D, N).contiguous()
+    x["x"][:, :first] = 0
+    x["dt"][:, :first] = 2
+    seg = (torch.arange(T, device="cuda") >= first).int().expand(2, T).contiguous()
+    dy, dso = incoming(2, T, D, N, F)
+    dy[:, :first] = 0
+    y, st, sv = forward(x, segments=seg, y_dtype=F, save=True)
+    g = backward(x, dy, dso, sv, segments=seg, grad_dtype=F)
+    out, bound = oracle(x, dy, dso, segments=seg)
+    for n, got in dict(g, y=y, state_out=st).items():
+        check(n, got, out[n], bound[n])
+
+
 def shifted(t, off):
     """t in an allocation of its own, `off` elements into it, NaN around."""
     flat = torch.full((t.numel() + 16,), math.nan, dtype=t.dtype, device="cuda")
