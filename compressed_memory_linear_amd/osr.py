@@ -1215,6 +1215,8 @@ def lattice_osr_ssm_step(x, dt, A, B, C, state_in, *, D=None, z=None, dt_bias=No
     """One token of lattice_osr_ssm_fwd (T = 1) for every sequence; state_out may be state_in (in place).
     Returns (y, state_out)."""
     lib = load_library()
+    if state_in is None:
+        raise ValueError("state_in: the state of every sequence (zeros at its start)")
     fields, sshape = _ssm_desc(x, dt, A, B, C, D, z, dt_bias, softplus, None, None, y_dtype, torch.float32)
     dev = x.device
     _check_tensor("state_in", state_in, sshape, torch.float32, dev)

@@ -261,6 +261,7 @@ def test_ssm_binding_checks():
     _raises("GPU", g, **a, dy=_z(B, T, D), saved=saved)
     s = osr.lattice_osr_ssm_step
     _raises("state_in has shape", s, **a, state_in=_z(B, D, dtype=f32))
+    _raises("state_in: the state", s, **a, state_in=None)
     _raises("GPU", s, **a, state_in=_z(B, D, N, dtype=f32))
 
 
