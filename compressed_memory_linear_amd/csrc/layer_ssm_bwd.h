@@ -18,7 +18,7 @@
 // instructions per state and token six take the state again, nine are the gradients' and five the sums over
 // channels, which permlane swaps of 8 cycles make 94 of 350 cycles per token and four states.  The maps in front 95 us, the
 // kernels behind 14 and 8.  (The whole training step: 4825 us with one wave's sums over 64 lanes one by one, one
-// segment and nothing ahead; 945 so.)  64 states (B3 T777 D514 fp32) spill 131 to 153 registers: 248 us,
+// segment and nothing ahead; 945 so.)  64 states (B3 T777 D514 fp32) spill 107 to 145 registers: 239 us,
 // with the decays held too 334, in one part of 16 tokens 400.
 #pragma once
 
@@ -425,6 +425,9 @@ struct Walker {
                     for (int n = 0; n < SN; ++n) mid[n] = fmaf(decay(d, n), cut ? 0.0f : mid[n], bcast<t>(Bv[n]) * u);
                 });
             }
+            // (Eight states to a lane: tokens of the way back stay apart, and on the way forward where rows move element by
+            // element, since what the compiler takes ahead it spills.  B4 T2048 D1024 N64 fp32 1083 us without, 928
+            // so, 957 with both; B3 T777 D514, odd rows, 390, 383, 373.)
             each<kParts>([&](auto pc) {
                 constexpr int first = (kParts - 1 - pc()) * kPart;
                 const float(&start)[SN] = first ? mid : before;
@@ -449,6 +452,7 @@ struct Walker {
                             for (int n = 0; n < SN; n += 2 * k) y[n] += y[n + k];
                         sh.y[B][wave][t][l] = y[0];
                     }
+                    if constexpr (!kHold && !VEC) __builtin_amdgcn_sched_barrier(0);
                 });
                 float v[16];
                 each<kPart>([&](auto tc) {
@@ -480,6 +484,7 @@ struct Walker {
                         sh.part[B][wave][t][1][l] = q;
                     }
                     if constexpr (j == kPair - 1) (&sh.sums[B][t + kPair - 1][0])[sum_at] = sum16(v, l);
+                    if constexpr (!kHold) __builtin_amdgcn_sched_barrier(0);
                 });
             });
         });
