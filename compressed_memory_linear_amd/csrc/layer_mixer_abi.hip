@@ -43,10 +43,16 @@ int check_conv(const lattice_osr_conv_desc* d) {
     if (d->act != LATTICE_OSR_CONV_NONE && d->act != LATTICE_OSR_CONV_SILU) return LATTICE_OSR_ERR_UNSUPPORTED;
     if (!dtype_ok(d->in_dtype) || !dtype_ok(d->y_dtype) || !dtype_ok(d->grad_dtype)) return LATTICE_OSR_ERR_UNSUPPORTED;
     if (!row_ok(d->x_row, d->D)) return LATTICE_OSR_ERR_SHAPE;
-    // a launch has fewer than 2^32 threads: at most one for each channel and 16 tokens (their number also bounds
-    // the workgroups of the column sums)
+    // a launch has fewer than 2^32 threads: the forward's at most two for each channel and 16 tokens
     if ((static_cast<int64_t>(d->T) + 15) / 16 * d->B * d->D >= INT64_C(1) << 31) return LATTICE_OSR_ERR_SHAPE;
     return LATTICE_OSR_OK;
+}
+
+// The backward's launch has 64 threads to a run, whatever D is.
+int check_conv_bwd(const lattice_osr_conv_desc* d) {
+    const int rc = check_conv(d);
+    if (rc != LATTICE_OSR_OK) return rc;
+    return layer::conv_groups(d->B, d->T) < 1 << 26 ? LATTICE_OSR_OK : LATTICE_OSR_ERR_SHAPE;
 }
 
 layer::ConvParams conv_params(const lattice_osr_conv_desc* d) {
@@ -142,7 +148,7 @@ bool ln_vec(const lattice_osr_layernorm_desc* d, const Buf* b, int n) {
 extern "C" {
 
 size_t lattice_osr_conv_bwd_workspace_bytes(const lattice_osr_conv_desc* desc) {
-    return check_conv(desc) != LATTICE_OSR_OK ? static_cast<size_t>(-1) : conv_part_bytes(desc);
+    return check_conv_bwd(desc) != LATTICE_OSR_OK ? static_cast<size_t>(-1) : conv_part_bytes(desc);
 }
 
 int lattice_osr_conv_fwd(const lattice_osr_conv_desc* desc, const void* x, const float* w, const float* bias,
@@ -176,7 +182,7 @@ int lattice_osr_conv_bwd(const lattice_osr_conv_desc* desc, const void* x, const
                          const int32_t* lengths, const int32_t* segments, const void* hist_in, const void* dy,
                          const void* dhist_out, void* dx, float* dw, float* dbias, void* dhist_in, void* workspace,
                          size_t workspace_bytes, void* hip_stream) {
-    int rc = check_conv(desc);
+    int rc = check_conv_bwd(desc);
     if (rc != LATTICE_OSR_OK) return rc;
     if (!x || !w || !dy || !dx) return LATTICE_OSR_ERR_NULL;
     const bool sums = dw || dbias;

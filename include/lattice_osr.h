@@ -575,6 +575,7 @@ LATTICE_OSR_API size_t lattice_osr_norm_bwd_workspace_bytes(const lattice_osr_no
  *                      to the first token's document, and rows of hist_out that lie before the
  *                      last token's document are zeros.
  * W is 1 to 8 (1: no history, whose buffers are then not used), D up to 2^20.
+ * B D ceil(T / 16) must stay below 2^31, for the backward B ceil(T / 128) below 2^26 too.
  */
 #define LATTICE_OSR_CONV_NONE 0
 #define LATTICE_OSR_CONV_SILU 1

@@ -200,6 +200,24 @@ def test_size_limits():
         osr.lattice_osr_conv_bwd_workspace_bytes(osr.make_conv_desc(1, 1 << 30, 32, 4))
 
 
+@pytest.mark.parametrize("B,T,D", [(1 << 26, 1, 16), (1 << 26, 128, 1), ((1 << 26) - 1, 129, 1), (1 << 19, 1 << 14, 3),
+                                   ((1 << 31) - 1, 1, 1)])
+def test_convolution_backward_runs(B, T, D):
+    """B ceil(T / 128) runs of 64 threads each are a launch of fewer than 2^32, whatever D is: what has more of them is
+    refused by the backward and its workspace query before anything is asked for, and taken by the forward."""
+    assert B * -(-T // 128) >= 1 << 26 and B * -(-T // 16) * D < 1 << 31
+    d = osr.make_conv_desc(B, T, D, 1)
+    # buffers further apart than the largest of them
+    far = lambda fn: {n: BASE + i * (1 << 44) for i, n in enumerate(NAMES[fn])}
+    assert call("conv_bwd", d, far("conv_bwd"), ws=1 << 50) == SHAPE
+    with pytest.raises(osr.OSRError):
+        osr.lattice_osr_conv_bwd_workspace_bytes(d)
+    p = far("conv_fwd")
+    assert call("conv_fwd", d, {**p, "y": p["x"]}) == osr.ERR_ALIAS  # past the check of the sizes
+    inside = osr.make_conv_desc((1 << 26) - 1, 1, 16, 1)
+    assert osr.lattice_osr_conv_bwd_workspace_bytes(inside) == ((1 << 26) - 1) * 2 * 16 * 4
+
+
 # -------------------------------------------------------------- binding --
 B, T, D, N = 2, 6, 24, 5
 BF = torch.bfloat16
