@@ -33,12 +33,16 @@ __device__ __forceinline__ void softplus_parts(float v, float& d, float& slope) 
     slope = v < 0.0f ? e * r : r;
 }
 
-// A state (or a gradient) h across a segment of the time axis: exp(A S) h + H, with the segment's sum of steps S and
-// what it makes of zeros, H.  A segment with a document's border in it (S = inf) passes nothing on, whatever it is.  The
+// A state (or a gradient) h across a segment of the time axis: exp(A sum) h + H, with the sum of the segment's steps and
+// what it makes of zeros, H.  S is the sum times 2^-31, so that no sum of up to 2^30 finite steps is infinite.  A
+// segment with a document's border in it (S = inf) passes nothing on, whatever it is.  The
 // decay goes in two halves, each kept between the least and the largest float: an infinite h stays one where the
 // product of decays underflows and a zero stays one where growth (A > 0) overflows, as token by token.
+__device__ __forceinline__ float ssm_steps(double sum, bool dropped) {
+    return dropped ? __builtin_inff() : static_cast<float>(sum * 0x1p-31);
+}
 __device__ __forceinline__ float ssm_across(float A, float S, float h, float H) {
-    const float P = fminf(fmaxf(__builtin_amdgcn_exp2f(0.5f * (A * S)), 1.40129846e-45f), 3.40282347e38f);
+    const float P = fminf(fmaxf(__builtin_amdgcn_exp2f(0x1p30f * (A * S)), 1.40129846e-45f), 3.40282347e38f);
     return S == __builtin_inff() ? H : fmaf(P * h, P, H);
 }
 

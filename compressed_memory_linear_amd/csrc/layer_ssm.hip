@@ -311,7 +311,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
             const double* sums = reinterpret_cast<const double*>(&du[0][0][0][0]);
             double s = 0.0;
             for (int j = 0; j < HT / 16; ++j) s += sums[j * 64 + l];
-            m[NP * 64] = dropped ? __builtin_inff() : static_cast<float>(s);
+            m[NP * 64] = ssm_steps(s, dropped);
         }
     } else if (p.state_out && me.live && seg == ws.segs - 1) {
 #pragma unroll

@@ -157,7 +157,7 @@ __global__ __launch_bounds__((NW + (NW < 4 ? 2 : 4)) * 64) void layer_ssm_bwd_ma
         const double* sums = reinterpret_cast<const double*>(&in[0][0][0][0]);
         double a = 0.0;
         for (int j = 0; j < HT / 16; ++j) a += sums[j * 64 + l];
-        m[NP * 64] = dropped ? __builtin_inff() : static_cast<float>(a);
+        m[NP * 64] = ssm_steps(a, dropped);
     }
 }
 

@@ -234,6 +234,28 @@ def test_states_that_grow(D, N, dtype):
         check(n, got, out[n], bound[n])
 
 
+@pytest.mark.parametrize("D,N", [(66, 4), (64, 33)])
+def test_sums_of_steps_past_fp32(D, N):
+    """Steps of 5e36 to 8e36 beside decays of 0 and 1.2e-38 up: each step is finite and takes a state on by 0 to some
+    tenths, but the sum over a segment (80 tokens) passes fp32's range.  It is not taken for a border."""
+    T = 160
+    g = torch.Generator(device="cuda").manual_seed(22)
+    r = lambda *s: torch.randn(s, generator=g, device="cuda")
+    x = make(2, T, D, N, dtype=F, seed=21, bias=False)
+    x["dt"] = 5e36 + 3e36 * torch.rand((2, T, D), generator=g, device="cuda")
+    x["x"] = 1e-37 * r(2, T, D)
+    x["A"] = torch.linspace(0, -6e-38, N, device="cuda").expand(D, N).contiguous()
+    x["A"][:, 1:] -= 1.2e-38
+    seg = (torch.arange(T, device="cuda") >= 120).int() * torch.tensor([[0], [1]], device="cuda")
+    seg = seg.int().contiguous()  # the second row has a border in its last segment
+    dy, dso = 1e-3 * r(2, T, D), 1e-3 * r(2, D, N)
+    y, st, sv = forward(x, softplus=False, segments=seg, save=True)
+    got = dict(backward(x, dy, dso, sv, softplus=False, segments=seg), y=y, state_out=st)
+    out, bound = oracle(x, dy, dso, softplus=False, segments=seg)
+    for n in got:
+        check(n, got[n], out[n], bound[n])
+
+
 def shifted(t, off):
     """t in an allocation of its own, `off` elements into it, NaN around."""
     flat = torch.full((t.numel() + 16,), math.nan, dtype=t.dtype, device="cuda")
