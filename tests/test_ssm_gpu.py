@@ -390,6 +390,38 @@ def test_step(B, D, N, G, dtype, y_dtype):
         assert torch.equal(y2, y) and torch.equal(inplace, st)
 
 
+@pytest.mark.parametrize("B", [16, 17, 18, 19, 31])
+@pytest.mark.parametrize("D,N,G", [(130, 16, 2), (33, 5, 1), (64, 64, 1)])
+def test_step_of_batches_with_a_remainder(B, D, N, G):
+    """From 16 sequences on a thread takes four of them: the last has fewer.  Into buffers of their own with NaN around,
+    and in place."""
+    x = make(B, 1, D, N, G, seed=38)
+    out, bound = oracle(x)
+    (yf, y), (sf, so) = (shifted(torch.zeros(s, dtype=t, device="cuda"), 8) for s, t in (((B, 1, D), BF), ((B, D, N), F)))
+    step(x, y_dtype=BF, y=y, state_out=so)
+    check("y", y, out["y"], bound["y"])
+    check("state", so, out["state_out"], bound["state_out"])
+    for flat, v in ((yf, y), (sf, so)):
+        assert torch.isnan(flat[:8]).all() and torch.isnan(flat[8 + v.numel():]).all()
+    inplace = x["state_in"].clone()
+    y2, _ = step(dict(x, state_in=inplace), y_dtype=BF, state_out=inplace)
+    assert torch.equal(y2, y) and torch.equal(inplace, so)
+
+
+@pytest.mark.parametrize("B,T,D,N,G", [(1, 1030, 8192, 16, 1), (2, 1060, 4100, 13, 2), (1, 1040, 8191, 8, 1),
+                                       (1, 1100, 4096, 24, 1)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_segments_of_several_parts(B, T, D, N, G, dtype):
+    """Backward segments of sixteen tiles or more, which come in four parts with a map each, at every number of waves but
+    those of test_long_and_wide."""
+    g = torch.Generator(device="cuda").manual_seed(42)
+    x = make(B, T, D, N, G, dtype, seed=42, step=0.01)
+    n = torch.tensor([T - 100, 700][:B], dtype=torch.int32, device="cuda")
+    seg = (torch.rand((B, T), generator=g, device="cuda") < 3 / T).cumsum(1).int()
+    run_all(x, y_dtype=dtype, grad_dtype=dtype)
+    run_all(x, y_dtype=dtype, grad_dtype=dtype, lengths=n, segments=seg)
+
+
 @pytest.mark.parametrize("B,T,D,N,G", [(1, 5000, 64, 16, 1), (1, 2500, 320, 16, 1), (2, 2100, 128, 32, 2),
                                        (1, 1300, 130, 64, 1), (9, 600, 512, 16, 1), (1, 1300, 6400, 4, 1),
                                        (1, 1030, 4096, 33, 1)])
@@ -558,3 +590,24 @@ def test_offsets_past_32_bits():
     check("state", st[:, cols].contiguous(), out["state_out"], bound["state_out"])
     for k in ("dx", "ddt", "dz"):
         check(k, g[k][:, cut:, cols].contiguous(), out[k], bound[k])
+
+
+def test_sums_past_32_bits():
+    """The partial sums of B's and C's gradients in more than 2^31 words of workspace, the last words being those of the
+    only channels that a gradient reaches: all sums are those of these channels alone."""
+    T, D, N = 2100, 16384 * 32, 64
+    assert (D // 64) * T * 2 * N > 2 ** 31
+    x = make(1, T, D, N, seed=63, state=False)
+    cols = slice(D - 64, D)
+    dy = torch.zeros((1, T, D), dtype=BF, device="cuda")
+    dy[..., cols] = torch.randn((1, T, 64), device="cuda").to(BF)
+    y, st, sv = forward(x, save=True, y_dtype=BF)
+    g = backward(x, dy, None, sv, grad_dtype=BF)
+    part = {k: t[..., cols].contiguous() if k in ("x", "dt", "z", "D", "dt_bias") else t for k, t in x.items()}
+    part["A"] = x["A"][cols].contiguous()
+    out, bound = oracle(part, dy[..., cols].contiguous())
+    for k in ("dB", "dC"):
+        check(k, g[k], out[k], bound[k])
+    for k in ("dA", "dD", "ddt_bias"):
+        check(k, g[k][cols], out[k], bound[k])
+        assert (g[k][:D - 64] == 0).all(), k
