@@ -33,6 +33,12 @@ __device__ __forceinline__ void softplus_parts(float v, float& d, float& slope) 
     slope = v < 0.0f ? e * r : r;
 }
 
+// What the kernels hold of a decay: A log2(e), kept finite where A is (a step of zero keeps the state, whatever A).
+__device__ __forceinline__ float ssm_decay(float a) {
+    const float v = a * kLog2e;
+    return fabsf(v) == __builtin_inff() ? __builtin_copysignf(3.40282347e38f, v) : v;
+}
+
 // A state (or a gradient) h across a segment of the time axis: exp(A sum) h + H, with the sum of the segment's steps and
 // what it makes of zeros, H.  S is the sum times 2^-31, so that no sum of up to 2^30 finite steps is infinite.  A
 // segment with a document's border in it (S = inf) passes nothing on, whatever it is.  The

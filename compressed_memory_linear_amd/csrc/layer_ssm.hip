@@ -206,7 +206,7 @@ __global__ __launch_bounds__((NW + kHelpers<NW>) * 64) void layer_ssm_fwd_kernel
 #pragma unroll
     for (int n = 0; n < SN; ++n) {
         const bool on = n0 + n < p.N;
-        A[n] = on ? p.A[static_cast<int64_t>(c) * p.N + n0 + n] * kLog2e : 0.0f;
+        A[n] = on ? ssm_decay(p.A[static_cast<int64_t>(c) * p.N + n0 + n]) : 0.0f;
         h[n] = on && p.state_in && (MAPS ? seg == 0 : ws.segs == 1) ? p.state_in[state + n] : 0.0f;
     }
     if constexpr (MAPS) {
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(256) void layer_ssm_step_kernel(SsmParams p) {
             float y[1] = {0.0f}, o[4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
-                o[n] = fmaf(__builtin_amdgcn_exp2f(d * (A.e[n] * kLog2e)), h[i].e[n], u * widen(B[i].e[n]));
+                o[n] = fmaf(__builtin_amdgcn_exp2f(d * ssm_decay(A.e[n])), h[i].e[n], u * widen(B[i].e[n]));
                 if (n < left) y[0] = fmaf(widen(C[i].e[n]), o[n], y[0]);
             }
             y[0] = osr::group_sum<L>(y[0]);

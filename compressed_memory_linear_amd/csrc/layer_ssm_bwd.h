@@ -356,7 +356,7 @@ struct Walker {
         for (int n = 0; n < SN; ++n) {
             // (lanes past the last channel hold zeros throughout, since the sums over channels take them in)
             const bool on = n0 + n < p.N && me.live;
-            A[n] = on ? p.A[static_cast<int64_t>(c) * p.N + n0 + n] * kLog2e : 0.0f;
+            A[n] = on ? ssm_decay(p.A[static_cast<int64_t>(c) * p.N + n0 + n]) : 0.0f;
             lam[n] = on && p.dstate_out ? p.dstate_out[state + n] : 0.0f;
         }
         for (int k = ws.parts - 1; k >= (s.seg + 1) * ws.per; --k) {

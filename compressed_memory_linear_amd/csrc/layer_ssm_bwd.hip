@@ -107,7 +107,7 @@ __global__ __launch_bounds__((NW + (NW < 4 ? 2 : 4)) * 64) void layer_ssm_bwd_ma
     float A[SN], r[SN] = {};
 #pragma unroll
     for (int n = 0; n < SN; ++n)
-        A[n] = n0 + n < p.N && me.live ? p.A[static_cast<int64_t>(me.c) * p.N + n0 + n] * kLog2e : 0.0f;
+        A[n] = n0 + n < p.N && me.live ? ssm_decay(p.A[static_cast<int64_t>(me.c) * p.N + n0 + n]) : 0.0f;
     SsmRegs<TIn, SN, VEC> nc[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) nc[k].place(l, n0, p.N, p.c_row);

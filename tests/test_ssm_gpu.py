@@ -256,6 +256,28 @@ def test_sums_of_steps_past_fp32(D, N):
         check(n, got[n], out[n], bound[n])
 
 
+@pytest.mark.parametrize("D,N", [(66, 4), (64, 40)])
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_decays_of_the_lowest_value(D, N, dtype):
+    """A of fp32's lowest value, which log2(e) takes past its range: such a state holds the last token's input alone, is
+    kept by padding and by steps of zero, and has gradients of zero."""
+    T, lowest = 150, torch.finfo(F).min
+    x = make(2, T, D, N, dtype=dtype, seed=64)
+    x["A"][:, ::3] = lowest
+    n = torch.tensor([T, 70], dtype=torch.int32, device="cuda")
+    run_all(x, lengths=n)
+    zero = dict(x, dt=torch.zeros_like(x["dt"]), dt_bias=None)
+    y, st = forward(zero, softplus=False)
+    out, bound = oracle(zero, softplus=False)
+    check("y of steps of zero", y, out["y"], bound["y"])
+    assert torch.equal(st, x["state_in"])
+    one = {k: t[:, :1].contiguous() if k in ("x", "dt", "z", "B", "C") else t for k, t in zero.items()}
+    out, bound = oracle(one, softplus=False)
+    y, st = step(one, softplus=False)
+    check("y of one step of zero", y, out["y"], bound["y"])
+    assert torch.equal(st, x["state_in"])
+
+
 def shifted(t, off):
     """t in an allocation of its own, `off` elements into it, NaN around."""
     flat = torch.full((t.numel() + 16,), math.nan, dtype=t.dtype, device="cuda")
