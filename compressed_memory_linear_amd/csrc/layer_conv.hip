@@ -1,7 +1,7 @@
 // layer_conv.hip -- the short causal convolution in front of a recurrence: forward and single step (layer_conv.h).
 //
-// Bound by HBM: B8 T4096 D2048 W4 bf16 moves 268 MB in 53 us, 5.1 TB/s (a token at a time, its row asked for
-// when it is needed, 68).  One token of one sequence: 3 us, and 9 for the host's call.
+// Bound by HBM: B8 T4096 D2048 W4 bf16 moves 268 MB in 48 to 61 us, 4.4 to 5.6 TB/s, fp32 twice that in 107, 5.0 TB/s
+// (bf16 a token at a time, its row asked for when it is needed, 68).  One token of one sequence: 3 us, and 9 for the host's call.
 #include "layer_conv.h"
 
 namespace layer {

@@ -17,7 +17,7 @@ using layer::check_buffers;
 using layer::dtype_ok;
 using layer::elem;
 
-constexpr int kMaxRow = 1 << 22;  // elements from row to row: 32 rows of floats stay under 2^30 bytes
+constexpr int kMaxRow = 1 << 22;  // elements from row to row: a tile's 16 rows of floats stay under 2^30 bytes
 
 bool row_ok(int row, int64_t width) { return row == 0 || (row >= width && row <= kMaxRow); }
 int row_of(int row, int width) { return row ? row : width; }

@@ -17,7 +17,7 @@ constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 // softplus(v) and its derivative.  With e = exp(-|v|) in [0, 1], softplus = max(v, 0) + log(1 + e) and
 // log(1 + e) = 2 atanh(t), t = e / (2 + e) <= 1/3: an odd polynomial of degree 9, the nearest in relative
-// error (4e-9, fitted for this by reweighted least squares), so that small steps keep their relative accuracy.
+// error (7.8e-9, fitted for this by reweighted least squares), so that small steps keep their relative accuracy.
 template <bool ACC>
 __device__ __forceinline__ void softplus_parts(float v, float& d, float& slope) {
     const float e = exp_of<ACC>(-fabsf(v));
@@ -229,6 +229,7 @@ __host__ __device__ inline int ssm_padded(int N) { return N <= 4 ? 4 : N <= 8 ? 
 // 149, 6 130, 9 122.  Past 32 states a wave holds twice as many: training step of B3 T777 D514 N64 with 7 segments
 // forward 427 us, 10 471.  Backward, by workgroups, of which a compute unit's LDS holds one past 8 states: training step
 // of B4 T4096 D2048 N16 (128 chains) 2 segments 1000 us, 4 970, 8 980; B3 T777 D514 N64 (30 chains) 4 749, 8 529, 12 597.
+// Past 176 chains there is one: 256 of them (B8 T4096 D2048) take 1137 us, 288 (B9) two rounds of the device and 2235.
 // The kernel of its maps has smaller workgroups and takes long segments in four parts (B4 T4096, 64 tiles a segment:
 // 128 -> 95 us), short ones whole, since each segment reads the maps of all parts behind it (the training step of
 // B3 T777, 7 tiles a segment: whole 393 us, in four parts 427).

@@ -11,7 +11,8 @@
 // busy throughout.  From a wave for all 16 states and B and C in LDS, a tile at a time (1099 and 17400 us): segments, B and C by lane
 // broadcast, quads 433 and 1430; addresses kept, steps four tokens ahead 395; inputs and outputs by waves of their own 390 and
 // 920; loads two tiles ahead 320 and 870.  Two states to a lane and twice the waves: 332 and 1071 with one
-// and 8 segments, against 317 and 1049.
+// and 8 segments, against 317 and 1049.  Tiles behind a sequence's end are computed as the others are, with steps of zero:
+// B7 T1531 D1001 N13 fp32 takes 144 us at full lengths, 117 at half of them and 89 with no token at all.
 #include "layer_ssm.h"
 
 namespace layer {

@@ -18,8 +18,10 @@
 // instructions per state and token six take the state again, nine are the gradients' and five the sums over
 // channels, which permlane swaps of 8 cycles make 94 of 350 cycles per token and four states.  The maps in front 95 us, the
 // kernels behind 14 and 8.  (The whole training step: 4825 us with one wave's sums over 64 lanes one by one, one
-// segment and nothing ahead; 945 so.)  64 states (B3 T777 D514 fp32) spill 107 to 145 registers: 239 us,
-// with the decays held too 334, in one part of 16 tokens 400.
+// segment and nothing ahead; 945 so.)  Past 16 states, where the
+// threads that walk take inputs too, a tile's inputs on their way lie in registers across the walk, which spill: 32 to 76
+// of them up to 32 states, 91 to 145 up to 64 (4 to 18 at 16).  64 states (B3 T777 D514 fp32): 239 us, with the decays held
+// too 334, in one part of 16 tokens 400.
 #pragma once
 
 #include "layer_ssm.h"

@@ -893,7 +893,8 @@ def lattice_osr_norm_bwd(y=None, x=None, dx_out=None, dz=None, *, gate=None, gat
 def _row(name, t, shape, dtype, dev, inner):
     """Elements from one token's row of t to the next (0: contiguous), after checking its shape, dtype and
     device: t is [B,T,...] whose last `inner` dimensions are contiguous and whose rows
-    are one stride apart, as a slice of the last dimension of a contiguous tensor is."""
+    are one stride apart, as a slice of the last dimension of a contiguous tensor is.  (The library takes strides of
+    up to 2^22 elements; one token of each of several long sequences can lie further apart, and has to be copied.)"""
     if t.is_contiguous():
         if t.shape == shape and t.dtype is dtype and t.device == dev:
             return 0
@@ -980,8 +981,8 @@ def lattice_osr_conv_fwd(x, w, bias=None, hist_in=None, *, act: int = CONV_SILU,
                          y_dtype=None, y=None, hist_out=None, return_history: bool = False, stream=None):
     """p_t = bias + sum_j w[j] x_{t-W+1+j} per channel, y = p sigmoid(p) (act CONV_SILU) or p (CONV_NONE).
 
-    x [B,T,D] or [B,T,H,d] (float32 or bfloat16; its rows may be a stride apart, as in a slice of a
-    projection's output), w [D,W] and bias [D] float32; hist_in [B,W-1,D] in x's dtype, the raw rows before
+    x [B,T,D] or [B,T,H,d] (float32 or bfloat16; its rows may be a stride of up to 2^22 elements apart, as in a slice of
+    a projection's output), w [D,W] and bias [D] float32; hist_in [B,W-1,D] in x's dtype, the raw rows before
     the first token (None: zeros); lengths [B] int32: the tokens of each sequence, y is zero behind them; segments
     [B,T] int32: the document of every token, whose border no tap crosses.  y has x's shape, in y_dtype (x's
     dtype if None).  Returns y and, with return_history (or `hist_out`), the raw rows behind the last
@@ -1137,7 +1138,7 @@ def lattice_osr_ssm_fwd(x, dt, A, B, C, state_in=None, *, D=None, z=None, dt_bia
     sum itself), y_t = (sum_n C_t h_t + D x_t) z_t sigmoid(z_t) (no gate without z).
 
     x, dt, z [B,T,D] or [B,T,H,d] and B, C [B,T,N] or [B,T,G,N] (channel c takes group c // (D/G)) share a
-    dtype, float32 or bfloat16; rows may be a stride apart, as in a slice of a projection's output.  A [D,N],
+    dtype, float32 or bfloat16; rows may be a stride of up to 2^22 elements apart, as in a slice of a projection's output.  A [D,N],
     D and dt_bias [D] are float32, state_in (None: zeros) and state_out [B,D,N] too, state_out may be
     state_in; lengths [B] int32: the tokens of each sequence, y is zero behind them; segments [B,T] int32: the
     document of every token, at whose borders the state starts from zero.

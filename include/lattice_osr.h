@@ -686,7 +686,8 @@ LATTICE_OSR_API int lattice_osr_ssm_fwd(const lattice_osr_ssm_desc* desc, const 
  *   dA [D, N], dskip [D], ddt_bias [D]  float32; dskip, ddt_bias only where skip,
  *                dt_bias are; each NULL where it is not wanted
  *   dstate_in  [B, D, N] float32, or NULL (not wanted)
- * workspace: lattice_osr_ssm_bwd_workspace_bytes(desc) bytes, as the forward's.
+ * workspace: lattice_osr_ssm_bwd_workspace_bytes(desc) bytes, as the forward's;
+ * mostly the partial sums of dB and dC, 8 N bytes per token and 64 channels.
  */
 LATTICE_OSR_API int lattice_osr_ssm_bwd(const lattice_osr_ssm_desc* desc, const void* x, const void* dt,
                                         const float* A, const void* Bm, const void* Cm, const float* skip,
