@@ -261,3 +261,29 @@ def test_long_and_wide(B, T, D):
     g = torch.Generator(device="cuda").manual_seed(3)
     seg = (torch.rand((B, T), generator=g, device="cuda") < 20 / T).cumsum(1).int()
     run_all(make(B, T, D, seed=43), y_dtype=BF, grad_dtype=BF, segments=seg)
+
+
+def test_most_runs_of_the_backward():
+    """One run of 64 threads less than a launch of 2^32 has.  Whole numbers of unit size, so that every sum is exact
+    (a thread adds 2^21 of them): dx is the filter's last tap times dy, dw and dbias are counts."""
+    B = (1 << 26) - 1
+    g = torch.Generator(device="cuda").manual_seed(71)
+    r = lambda: torch.randint(-1, 2, (B, 1, 1), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    x, dy, hist = r(), r(), r()
+    w, bias = torch.tensor([[2.0, -3.0]], device="cuda"), torch.ones(1, device="cuda")
+    got = osr.lattice_osr_conv_bwd(x, w, dy, bias, hist, act=osr.CONV_NONE, grad_dtype=BF)
+    assert torch.equal(got["dx"], -3 * dy) and torch.equal(got["dhist_in"], 2 * dy)
+    count = lambda t: int(t.sum(dtype=torch.float64))
+    assert got["dw"].tolist() == [[count(dy * hist), count(dy * x)]] and got["dbias"].tolist() == [count(dy)]
+
+
+def test_widest_launch_of_the_forward():
+    """65 channels take two waves to a run, the most lanes that idle: a launch of nearly 2^32 threads.  Whole numbers
+    of up to 17, exact in bf16."""
+    D = 65
+    B = ((1 << 31) - 1) // D
+    g = torch.Generator(device="cuda").manual_seed(73)
+    x = torch.randint(-8, 9, (B, 1, D), generator=g, device="cuda", dtype=torch.int8).to(BF)
+    w = torch.ones((D, 1), device="cuda") * 2
+    y = osr.lattice_osr_conv_fwd(x, w, torch.full((D,), 1.0, device="cuda"), act=osr.CONV_NONE)
+    assert torch.equal(y, 2 * x + 1)

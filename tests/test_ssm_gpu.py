@@ -633,3 +633,9 @@ def test_sums_past_32_bits():
     for k in ("dA", "dD", "ddt_bias"):
         check(k, g[k][cols], out[k], bound[k])
         assert (g[k][:D - 64] == 0).all(), k
+
+
+def test_most_chains():
+    """As many chains as a call may have, of twelve waves each in the forward: launches of 3.2e9 and 2.1e9 threads, and
+    sums over as many sequences."""
+    run_all(make((1 << 22) - 1, 1, 1, 64, dtype=F, seed=65))
